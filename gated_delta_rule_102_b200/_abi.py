@@ -32,7 +32,9 @@ EXPORTS = ("gdn_conv_update", "gdn_recurrent_step", "gdn_gated_rmsnorm", "gdn_de
            "gdn_decode_workspace_bytes", "gdn_decode_step_varlen", "gdn_decode_step_static_scratch",
            "gdn_decode_static_scratch_bytes", "gdn_spec_verify", "gdn_spec_commit", "gdn_in_proj", "gdn_out_proj",
            "gdn_decode_step_device_batch", "gdn_selftest_wait_timeout",
-           "gdn_check_slots_host", "gdn_status_string", "gdn_abi_version")
+           "gdn_check_slots_host", "gdn_status_string", "gdn_abi_version",
+           "gdn_qk_rope_append", "gdn_attn_decode", "gdn_attn_decode_workspace_bytes", "gdn_rope_inv_freq_host",
+           "gdn_pages_reserve", "gdn_pages_fork", "gdn_pages_free", "gdn_pages_compact", "gdn_copy_rows")
 
 
 class GdnConfig(ctypes.Structure):

@@ -1,0 +1,114 @@
+// Internal interface of the softmax-attention layer (norm + rotary + append, paged
+// attention, page tables, row copies) between the C-ABI layer and the kernel
+// launchers. Nothing here is exported.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace gdn {
+
+constexpr int GDN_DEVICE_ERR_PAGE_BIT = 16;
+
+// Heads of a token row: element (row, head, i) at ptr[row * row_stride + head * head_stride + i].
+struct Heads {
+    const uint16_t* ptr;
+    long row, head;
+};
+
+struct AttnShape {
+    int Hq, Hkv, d, G;  // G = Hq / Hkv query heads per key/value head
+    int R;              // rotated leading dimensions of a head
+    bool interleaved, fp8;
+    int page_size, window;
+    float norm_eps, norm_offset, rope_scale, sm_scale, softcap, k_scale, v_scale;
+};
+
+// One layer's pages and the tables that the layers share.
+struct PagedCache {
+    void* k;
+    void* v;
+    int num_pages;
+    const int32_t* table;  // [rows][max_pages]
+    int rows, max_pages;
+    const int32_t* seq_lens;  // [rows]
+};
+
+struct AppendArgs {
+    AttnShape sh;
+    PagedCache c;
+    int B, T, total;
+    const int32_t* cu;
+    Heads q, k, v;
+    const uint16_t* qw;
+    const uint16_t* kw;
+    const float* inv_freq;
+    const int32_t* slots;
+    uint16_t* q_out;
+    int32_t* err_flag;
+};
+
+struct AttnArgs {
+    AttnShape sh;
+    PagedCache c;
+    int B, T, total;
+    const int32_t* cu;
+    Heads q, gate;  // gate.ptr null: no gate
+    const int32_t* slots;
+    uint16_t* out;
+    float* lse;
+    int32_t* err_flag;
+    unsigned int* counters;  // workspace: kAttnMaxCtas zeroed counters, left zeroed
+    float* partial;          // workspace: two partial results per CTA
+};
+
+// CTAs of the attention kernel (one per SM, at most this many) and the workspace.
+constexpr int kAttnMaxCtas = 192;
+constexpr int kAttnMaxBatch = 2048;
+int attn_row_tile(int d, bool fp8, int rows);  // query rows of a work unit for `rows` rows per key/value head
+int attn_token_tile(int d, bool fp8, int rows);
+size_t attn_workspace_bytes(int d, bool fp8, int rows);
+
+cudaError_t launch_qk_rope_append(const AppendArgs& a, cudaStream_t stream);
+cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t stream);
+
+struct PageArgs {
+    int page_size, n;           // sequences (or parent/child pairs) of this call
+    const int32_t* slots;       // children for fork
+    const int32_t* src_slots;   // fork: parents
+    const int32_t* n_tokens;    // reserve: nullable per-sequence counts
+    int T;                      // reserve: the count where n_tokens is null
+    int32_t* table;
+    int rows, max_pages;
+    int32_t* seq_lens;
+    int32_t* refs;
+    int num_pages;
+    int32_t* copy_src;
+    int32_t* copy_dst;
+    int32_t* n_copies;
+    int32_t* remap;
+    int32_t* err_flag;
+};
+constexpr int kPagesMaxBatch = 2048;
+cudaError_t launch_pages_reserve(const PageArgs& a, cudaStream_t stream);
+cudaError_t launch_pages_fork(const PageArgs& a, cudaStream_t stream);
+cudaError_t launch_pages_free(const PageArgs& a, cudaStream_t stream);
+cudaError_t launch_pages_compact(const PageArgs& a, cudaStream_t stream);
+
+constexpr int kCopyMaxBuffers = 64;
+struct CopyArgs {
+    unsigned char* base[kCopyMaxBuffers];
+    long row_bytes[kCopyMaxBuffers];
+    long first_chunk[kCopyMaxBuffers + 1];  // chunks of a pair that the buffers before this one hold
+    int n_bufs, rows, n_max;
+    const int32_t* src;
+    const int32_t* dst;
+    const int32_t* n_dev;
+    int32_t* err_flag;
+};
+cudaError_t launch_copy_rows(CopyArgs& a, cudaStream_t stream);
+
+// The number of SMs of the current device (looked up once per device).
+cudaError_t device_sms(int* device, int* sms);
+
+}  // namespace gdn

@@ -69,6 +69,7 @@ typedef enum {
 #define GDN_DEVICE_ERR_TIMEOUT 2    /* a bounded wait inside the kernel ran out */
 #define GDN_DEVICE_ERR_SEQLEN 4     /* a token count (varlen) or accepted count (spec commit) out of range */
 #define GDN_DEVICE_ERR_BATCH 8      /* gdn_decode_step_device_batch: *B_dev outside [0, B_max] */
+#define GDN_DEVICE_ERR_PAGE 16      /* a page number outside the pool, no free page left, or a table row in use */
 
 typedef struct {
     int32_t num_k_heads; /* Hk */
@@ -334,6 +335,181 @@ gdn_status gdn_decode_step_static_scratch(const gdn_config* cfg, int32_t B, int3
 size_t gdn_decode_static_scratch_bytes(void);
 
 /*
+ * ---------------------------------------------------------------------------------
+ * The softmax-attention layers that alternate with GDN layers in a hybrid model, on a
+ * paged key/value cache ("metrale_model_layers/forward/qwen3_5/full_attention.rs": the
+ * per-head q/k RMSNorm, the rotary positions, the KV append, the decode attention and
+ * the sigmoid output gate). The conventions above hold, with these additions.
+ *
+ * Cache. k_pages, v_pages [num_pages][page_size][Hkv][d], bf16 or e4m3, one pair per
+ *   layer. page_table [table_rows][max_pages] int32 and seq_lens [table_rows] int32 are
+ *   shared by all layers and indexed by SLOT like the GDN pools: the token at position
+ *   p of slot s is row p % page_size of page page_table[s][p / page_size]. Entries that
+ *   hold no page are -1. seq_lens[s] is the number of tokens stored BEFORE the step:
+ *   gdn_qk_rope_append writes positions seq_lens[s] .. and gdn_attn_decode reads them
+ *   too, and neither changes seq_lens, so every layer of the step sees the same lengths;
+ *   the caller advances them once per step (by the accepted count after a speculative
+ *   step: positions past seq_lens are rewritten by the next append, which is all that
+ *   rewinding takes).
+ * Rows. With cu_seqlens NULL sequence i owns T token rows i*T ..; otherwise T is the
+ *   largest count (1..16) and sequence i owns rows cu_seqlens[i] .. cu_seqlens[i+1]-1,
+ *   as in gdn_decode_step_varlen (0 tokens: left untouched, which also serves padded
+ *   batches in a captured graph; counts or rows out of range: skipped,
+ *   GDN_DEVICE_ERR_SEQLEN). total_tokens: rows of the packed tensors (B*T without
+ *   cu_seqlens). A sequence whose slot is outside [0, table_rows) is skipped and
+ *   flagged GDN_DEVICE_ERR_SLOT_RANGE, one whose length is negative or does not fit
+ *   max_pages * page_size positions is skipped and flagged GDN_DEVICE_ERR_SEQLEN.
+ *   A page number outside [0, num_pages) is flagged GDN_DEVICE_ERR_PAGE and neither
+ *   read nor written. Slots of one call are distinct.
+ */
+enum { GDN_KV_BF16 = 0, GDN_KV_E4M3 = 1 };
+
+typedef struct {
+    int32_t num_q_heads;      /* Hq, a multiple of Hkv, Hq/Hkv <= 16; query head h reads kv head h / (Hq/Hkv) */
+    int32_t num_kv_heads;     /* Hkv */
+    int32_t head_dim;         /* d: 64, 128 or 256 */
+    int32_t rotary_dim;       /* R: the leading R dimensions of each head are rotated; even, 0..d */
+    int32_t rope_interleaved; /* 0: pairs (i, i + R/2); 1: pairs (2i, 2i + 1) */
+    int32_t page_size;        /* tokens per page, 1..65536 */
+    int32_t kv_dtype;         /* GDN_KV_BF16 or GDN_KV_E4M3 */
+    int32_t window;           /* 0: none; W: a token attends the last W positions, its own among them */
+    float norm_eps;           /* epsilon of the q/k RMSNorm, inside the root */
+    float norm_offset;        /* the norm's weight is norm_offset + w (0, or 1 for weights stored around zero) */
+    float rope_scale;         /* factor on cos and sin (long-context scaling); 0 selects 1 */
+    float sm_scale;           /* factor on q.k; 0 selects 1/sqrt(d) */
+    float softcap;            /* 0: none; c: a score x becomes c tanh(x / c) */
+    float k_scale, v_scale;   /* e4m3: a stored value times this is the value; 0 selects 1. bf16: 0 or 1 */
+} gdn_attn_config;
+
+typedef struct {
+    void* k_pages; /* [num_pages][page_size][Hkv][d] */
+    void* v_pages;
+    int32_t num_pages;
+    const int32_t* page_table; /* [table_rows][max_pages], 4-byte aligned */
+    int32_t table_rows;
+    int32_t max_pages;
+    const int32_t* seq_lens; /* [table_rows], 4-byte aligned */
+} gdn_kv_cache;
+
+/* Heads of token rows that need not be contiguous (slices of one projection): element
+ * (row, head, i) at ptr[row * row_stride + head * head_stride + i]. Strides in elements,
+ * multiples of 8, not negative; ptr 16-byte aligned. */
+typedef struct {
+    const uint16_t* ptr;
+    int64_t row_stride;
+    int64_t head_stride;
+} gdn_heads;
+
+/*
+ * RMSNorm of each q and k head, rotary positions and the cache append, one launch:
+ *   x <- x / sqrt(mean x^2 + norm_eps) * (norm_offset + w)        (w NULL: no norm)
+ *   pair (x_i, x_j) at position p, angle p * inv_freq[i], c and s its cosine and sine
+ *   times rope_scale: (x_i c - x_j s, x_j c + x_i s)
+ *   q [rows][Hq][d], k, v [rows][Hkv][d]   bf16
+ *   q_norm_w, k_norm_w [d] bf16            nullable
+ *   inv_freq [R/2] fp32                    may be NULL when R = 0
+ *   q_out [rows][Hq][d] bf16               contiguous
+ * k and v go to the cache (e4m3: value / scale, saturated, round to nearest even). The
+ * angle is formed and reduced in 64 bits, so positions of millions of tokens keep full
+ * precision. A token whose page is flagged still gets its q_out row.
+ */
+gdn_status gdn_qk_rope_append(const gdn_attn_config* cfg, const gdn_kv_cache* cache, int32_t B, int32_t T,
+                              const int32_t* cu_seqlens, int32_t total_tokens, const gdn_heads* q, const gdn_heads* k,
+                              const gdn_heads* v, const uint16_t* q_norm_w, const uint16_t* k_norm_w,
+                              const float* inv_freq, const int32_t* slots, uint16_t* q_out, int32_t* err_flag,
+                              void* stream);
+
+/*
+ * Attention of the new tokens over the cache (theirs included: append first), one
+ * launch. Token t of a sequence at position p = seq_lens[slot] + t attends positions
+ * 0..p (the last `window` of them): x = sm_scale q.k (capped), P = softmax(x),
+ *   out = (sum_j P_j v_j) * sigmoid(gate)                          (gate NULL: no gate)
+ *   lse [rows][Hq] fp32 nullable: the natural logarithm of the sum of exp(x)
+ *   q, gate [rows][Hq][d] bf16; out [rows][Hq][d] bf16, contiguous
+ *   workspace of gdn_attn_decode_workspace_bytes(cfg, B, T) bytes, zeroed by the caller
+ *            once before its first use; every call leaves its counters zeroed again.
+ *            Calls that may run at the same time on the GPU need separate workspaces;
+ *            one that is large enough serves any configuration.
+ * Values of keys and values past a sequence's end are never used (they may be NaN), and
+ * a non-finite value of a later drafted token does not reach the rows before it. Pages
+ * that lie wholly before every row's window are not read. B <= 2048. Results do not
+ * depend on timing: the split of the work and the order of every sum follow from the
+ * lengths alone. A sequence with a flagged page has unspecified outputs.
+ */
+gdn_status gdn_attn_decode(const gdn_attn_config* cfg, const gdn_kv_cache* cache, int32_t B, int32_t T,
+                           const int32_t* cu_seqlens, int32_t total_tokens, const gdn_heads* q, const gdn_heads* gate,
+                           const int32_t* slots, uint16_t* out, float* lse, int32_t* err_flag, void* workspace,
+                           void* stream);
+
+/* Bytes of the workspace of gdn_attn_decode (0 for a configuration it refuses). */
+size_t gdn_attn_decode_workspace_bytes(const gdn_attn_config* cfg, int32_t B, int32_t T);
+
+/*
+ * Host: rotation speeds inv_freq[i], i < rotary_dim/2, for gdn_qk_rope_append and the
+ * factor for gdn_attn_config.rope_scale.
+ *   factor 1: theta^(-2i/R).   linear (yarn = 0): the same divided by factor.
+ *   yarn = 1 (Peng et al., "YaRN", 2023): pairs that turn less than once over
+ *   original_len tokens are divided by factor, those that turn more than 32 times are
+ *   kept, a ramp in between; *rope_scale = 0.1 ln(factor) + 1 (1 otherwise).
+ */
+gdn_status gdn_rope_inv_freq_host(int32_t rotary_dim, double theta, double factor, int32_t yarn, int32_t original_len,
+                                  float* inv_freq, float* rope_scale);
+
+/*
+ * Page tables kept on the device. page_refs [num_pages] int32 counts the table entries
+ * that hold each page (0: free). A new page is always the lowest free one, given in the
+ * order of the call's sequences, so tables are reproducible. Tables start as -1,
+ * counters and lengths as 0. Slots of one call are distinct (children of a fork among
+ * themselves and from all parents; one parent may appear many times). page_table,
+ * seq_lens and page_refs are updated in place; copy lists are written in full.
+ * A bad slot is skipped and flagged GDN_DEVICE_ERR_SLOT_RANGE, a bad length or count
+ * GDN_DEVICE_ERR_SEQLEN, and GDN_DEVICE_ERR_PAGE flags a sequence that was skipped
+ * because no free page was left for it (then every later one of the call that needs
+ * pages is skipped too) or because its table row is in use.
+ * n (sequences of a call) <= 2048.
+ *
+ * reserve: gives slot i the pages for its next n_tokens[i] tokens (n_tokens NULL: T).
+ * fork:    child dst[i] becomes a copy of parent src[i]: whole pages are shared, a
+ *          partly filled last page is replaced by a new one, and copy_src[i], copy_dst[i]
+ *          [n] say which page to copy where (-1, -1: none). The child's row must be
+ *          empty. Reserved pages past the parent's length are not inherited.
+ * free:    releases every page of the rows and sets their lengths to 0 (a slot listed
+ *          twice is released once).
+ * compact: moves the pages in use to the front of the pool: copy_src, copy_dst
+ *          [num_pages] get the *n_copies moves (the rest -1; sources and destinations
+ *          never overlap), remap [num_pages] each page's new number (-1 for a free one),
+ *          and every row of the table and the counters follow.
+ */
+gdn_status gdn_pages_reserve(int32_t page_size, int32_t n, const int32_t* slots, const int32_t* n_tokens, int32_t T,
+                             int32_t* page_table, int32_t table_rows, int32_t max_pages, const int32_t* seq_lens,
+                             int32_t* page_refs, int32_t num_pages, int32_t* err_flag, void* stream);
+gdn_status gdn_pages_fork(int32_t page_size, int32_t n, const int32_t* src, const int32_t* dst, int32_t* page_table,
+                          int32_t table_rows, int32_t max_pages, int32_t* seq_lens, int32_t* page_refs,
+                          int32_t num_pages, int32_t* copy_src, int32_t* copy_dst, int32_t* err_flag, void* stream);
+gdn_status gdn_pages_free(int32_t n, const int32_t* slots, int32_t* page_table, int32_t table_rows, int32_t max_pages,
+                          int32_t* seq_lens, int32_t* page_refs, int32_t num_pages, int32_t* err_flag, void* stream);
+gdn_status gdn_pages_compact(int32_t* page_table, int32_t table_rows, int32_t max_pages, int32_t* page_refs,
+                             int32_t num_pages, int32_t* copy_src, int32_t* copy_dst, int32_t* n_copies,
+                             int32_t* remap, int32_t* err_flag, void* stream);
+
+/*
+ * Copies rows of up to 64 buffers at once, one launch: for each pair i < n (n_dev
+ * non-NULL: i < min(*n_dev, n)) row dst_ids[i] of every buffer becomes row src_ids[i].
+ * A buffer is an array of `rows` rows of row_bytes bytes (a multiple of 16): the pages of
+ * every layer's cache after a fork or a compaction, or the slots of the GDN state and
+ * conv pools. Pairs with a negative id are skipped, ids >= rows are skipped and flagged
+ * GDN_DEVICE_ERR_SLOT_RANGE (*n_dev outside [0, n]: GDN_DEVICE_ERR_BATCH, nothing
+ * copied). Destinations are distinct and none is a source.
+ */
+typedef struct {
+    void* base;
+    int64_t row_bytes;
+} gdn_copy_buffer;
+gdn_status gdn_copy_rows(const gdn_copy_buffer* buffers, int32_t n_buffers, int32_t rows, int32_t n,
+                         const int32_t* src_ids, const int32_t* dst_ids, const int32_t* n_dev, int32_t* err_flag,
+                         void* stream);
+
+/*
  * Self-test of the bounded waits inside every kernel of this library (the pages have no
  * counterpart): one GPU thread waits on a barrier phase that nothing completes, gives up
  * after limit_cycles cycles of its SM's clock (1 .. 2^40) and ORs GDN_DEVICE_ERR_TIMEOUT
@@ -353,7 +529,7 @@ gdn_status gdn_check_slots_host(const int32_t* slots_host, int32_t B, int32_t po
 const char* gdn_status_string(gdn_status status);
 
 /* ABI version of this header: (major << 16) | minor. */
-#define GDN_ABI_VERSION ((1 << 16) | 4)
+#define GDN_ABI_VERSION ((1 << 16) | 5)
 int32_t gdn_abi_version(void);
 
 #ifdef __cplusplus
