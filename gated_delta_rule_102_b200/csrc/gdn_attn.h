@@ -3,6 +3,7 @@
 // launchers. Nothing here is exported.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -107,6 +108,10 @@ struct CopyArgs {
     int32_t* err_flag;
 };
 cudaError_t launch_copy_rows(CopyArgs& a, cudaStream_t stream);
+
+// A tiled tensor map of bf16 values or bytes, swizzled over its inner dimension of 128 or 64 bytes.
+bool encode_tensor_map(CUtensorMap* m, bool bytes, int rank, void* ptr, const cuuint64_t* dims, const cuuint64_t* strides,
+                       const cuuint32_t* box, int inner_bytes);
 
 // The number of SMs of the current device (looked up once per device).
 cudaError_t device_sms(int* device, int* sms);

@@ -177,7 +177,7 @@ gdn_status gdn_attn_decode(const gdn_attn_config* cfg, const gdn_kv_cache* cache
         return GDN_ERR_MISALIGNED;
     // the kernel numbers its work units (token tiles of a row tile of a head) in 32 bits
     const int rows = T * a.sh.G, tt = gdn::attn_token_tile(a.sh.d, a.sh.fp8, rows), rt = gdn::attn_row_tile(a.sh.d, a.sh.fp8, rows);
-    const double tiles = (double)B * ceil((double)a.c.max_pages * a.sh.page_size / tt) * a.sh.Hkv * ((rows + rt - 1) / rt);
+    const double tiles = (double)B * (ceil((double)a.c.max_pages * a.sh.page_size / tt) + 8) * a.sh.Hkv * ((rows + rt - 1) / rt);
     if (tiles > 2.0e9) return GDN_ERR_UNSUPPORTED;
     a.B = B;
     a.T = T;

@@ -15,18 +15,22 @@
 // its share, so the workspace does not grow with the lengths.
 //
 // Within a CTA four warps load and eight compute. The ring holds slots of 16 KB, the keys
-// and values of 16 KS tokens; each loading warp fills every fourth slot by itself with
-// 16-byte asynchronous copies, each token row addressed through the page table (any page
-// size works), looks up the pages of its next slot meanwhile, and the one that meets a
-// unit's first slot also brings the unit's queries and its description. Rows past the
-// sequence are filled with zeros: what the pool holds there (NaN included) is never used.
-// The computing warps form WM row groups of 16 rows by 8 / WM token groups; a token group
-// takes every (8 / WM)-th slot and runs its own online softmax on it (scores and
-// probabilities never leave registers), so no warp waits for another one until a unit
-// ends, where the groups are joined through shared memory. The ring runs across units.
+// and values of ST tokens; each loading warp fills every fourth slot by itself and looks up
+// the pages of its next slot meanwhile, and the one that meets a unit's first slot also
+// brings the unit's queries and its description. When the page size is a multiple of 8 a
+// slot is a few TMA tiles (one for the keys and one for the values when a page holds whole
+// slots); any other page size takes 16-byte asynchronous copies, row by row. Both write
+// the same layout: atoms of 8 tokens by 128 bytes, 128-byte swizzle.
+// The computing warps form WM row groups of 16 rows by CS column halves by NG token groups.
+// A token group takes every NG-th slot of a unit and runs its own online softmax on it
+// (scores and probabilities never leave registers), so no warp waits for another one until
+// the unit ends, where the token groups are joined through shared memory; a short unit is
+// one group's alone. (At head size 256 two warps compute the same scores and half of the
+// output each: that halves the registers and the data to join, for 1.5 times the products.)
 //
 // Bound by HBM for few query rows: 2 G n flop for each byte of a bf16 cache (8 query heads
 // per key/value head, one token: 8 flop per byte). Every wait is bounded.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -42,45 +46,62 @@ namespace gdn {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kLoadWarps = 4, kComputeWarps = 8, kAttnThreads = (kLoadWarps + kComputeWarps) * 32;
+constexpr int kUnitCost = 4;  // what a unit costs beside its slots, in slots (its queries, the join, the output)
+constexpr int kSingle = 4;    // a piece of so many slots or fewer is one token group's alone
 
 // Geometry: D head size, WM row groups of 16 query rows.
 template <int D, bool FP8, int WM>
 struct Geo {
     static constexpr int ROWB = D * (FP8 ? 1 : 2);  // bytes of a token's key (value)
-    static constexpr int SLOTB = 16 * 1024;
-    static constexpr int ST = SLOTB / 2 / ROWB;     // tokens of a slot
+    static constexpr int SLOTB = 16 * 1024, HALF = SLOTB / 2;
+    static constexpr int ST = HALF / ROWB;          // tokens of a slot
     static constexpr int KS = ST / 16;
-    static constexpr int NG = 8 / WM;               // token groups
+    static constexpr int CS = D == 256 ? 2 : 1;     // column halves
+    static constexpr int ND = D / CS / 8;           // 8-column tiles of a warp's output
+    static constexpr int NG = kComputeWarps / (WM * CS);  // token groups
+    static constexpr int READERS = WM * CS;         // warps that read a slot
     static constexpr int BM = 16 * WM;
-    static constexpr int QB = BM * D * 2;           // bytes of a unit's queries
-    static constexpr int NQ = QB >= 32768 ? 2 : 3;  // units whose queries are held
+    static constexpr int QP = D * 2 + 16;           // bytes from one query row to the next: eight rows, eight bank groups
+    static constexpr int QB = BM * QP;
+    static constexpr int NQ = WM == 4 ? 2 : 3;      // units whose queries are held
     static constexpr int CPR = ROWB / 16;           // 16-byte chunks of a token row
-    static constexpr int CH = 32;                   // columns of the output joined at a time
-    static constexpr int JROW = CH + 8;             // floats of a joined row: eight rows, eight bank groups
-    static constexpr int JOINB = 2 * 8 * 16 * JROW * 4;  // two buffers
-    static constexpr int FIXED = 1024 + (2 * BM + 2 * 8 * 16) * 4;
+    static constexpr int JOINB = NG == 1 ? 0 : (kComputeWarps / 2) * 32 * ND * 16;
+    static constexpr int FIXED = 4096;              // everything small (checked at the launch)
     static constexpr int FIT = (227 * 1024 - (kAttnMaxBatch + 1) * 4 - FIXED - JOINB - NQ * QB) / SLOTB;
     static constexpr int SLOTS = FIT > 12 ? 12 : FIT;
-    static_assert(SLOTS >= 6 && KS >= 1, "ring");
+    static_assert(SLOTS >= 8 && KS >= 1 && NG >= 1, "ring");
 };
-constexpr int kLoadWarps = 4, kComputeWarps = 8, kAttnThreads = (kLoadWarps + kComputeWarps) * 32;
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
     const int n = valid ? 16 : 0;  // 0: the 16 bytes are filled with zeros and nothing is read
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int c3, int c4, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3, "
+        "%4}], [%5];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(c3), "r"(c4), "r"(bar)
+        : "memory");
+}
+// The matrix loads are not volatile, so that the compiler may move them between the products;
+// what keeps them behind the wait for their data and before its release is after_wait() on the
+// address that they use and before_release() on the accumulators that depend on them.
+__device__ __forceinline__ void after_wait(uint32_t& addr) { asm volatile("" : "+r"(addr)::"memory"); }
 template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+__device__ __forceinline__ void before_release(float (&acc)[N][4]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        asm volatile("" : "+f"(acc[i][0]), "+f"(acc[i][1]), "+f"(acc[i][2]), "+f"(acc[i][3])::"memory");
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+    asm("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr));
 }
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+    asm("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];\n"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr));
 }
@@ -88,14 +109,12 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
 template <bool HALF>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     if (HALF)
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
             "%2, %3};\n"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     else
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, "
             "%1, %2, %3};\n"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -122,19 +141,19 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Byte offset of 16-byte chunk c of token row r in a tile whose rows are CPR chunks: the
-// chunks of eight consecutive rows fall into different bank groups for every c.
+// Byte offset of 16-byte chunk c of token row r in a slot's keys (or values): atoms of eight
+// rows by 128 bytes in which chunk c is stored at c ^ (r % 8) (64-byte rows: two to a line,
+// c ^ (r / 2 % 4)), the swizzles that the TMA unit applies. Eight rows, eight bank groups.
 template <int CPR>
 __device__ __forceinline__ int chunk_at(int r, int c) {
-    if (CPR >= 8) return (r * CPR + (c ^ (r & 7))) * 16;
-    const int line = r >> 1, pos = ((r & 1) * 4 + c) ^ (line & 7);  // two 64-byte rows a line
-    return (line * 8 + pos) * 16;
+    if (CPR >= 8) return ((r >> 3) * (CPR / 8) + (c >> 3)) * 1024 + (r & 7) * 128 + (((c ^ r) & 7) << 4);
+    return r * 64 + (((c ^ (r >> 1)) & 3) << 4);
 }
 
 // A sequence as the schedule sees it.
 struct Seq {
     int n, first, past, slot;  // tokens of this call, their first row, tokens before them
-    int lo, tiles;             // first position any row attends, slots of tokens from there
+    int lo, base, tiles;       // first position any row attends, the slots' first position, slots
     int row_tiles;
 };
 
@@ -152,6 +171,7 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& p, int b, bool report) {
     }
     s.past = 0;
     s.lo = 0;
+    s.base = 0;
     if (s.n < 0 || s.n > p.T || s.first < 0 || s.first > p.total - s.n) {
         if (report && p.err_flag) atomicOr(p.err_flag, GDN_DEVICE_ERR_SEQLEN_BIT);
         s.n = 0;
@@ -168,17 +188,19 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& p, int b, bool report) {
         return s;
     }
     if (p.sh.window > 0 && s.past + 1 > p.sh.window) s.lo = s.past + 1 - p.sh.window;
-    s.tiles = (s.past + s.n - s.lo + ST - 1) / ST;
+    s.base = s.lo & ~(ST - 1);
+    s.tiles = (s.past + s.n - s.base + ST - 1) / ST;
     s.row_tiles = (s.n * p.sh.G + BM - 1) / BM;
     return s;
 }
 
-// A unit as the loading warps describe it to the computing ones.
-struct Unit {
-    Seq s;
-    int h, rt;         // key/value head, row tile
-    int tile, count;   // this CTA's piece: its first slot and how many
-    int lo;            // number of the unit's first slot in the launch
+// A CTA's piece of a unit, as the loading warps describe it to the computing ones.
+struct Piece {
+    int n, first, past, lo, base;  // of the sequence
+    int h, rt;                     // key/value head, row tile
+    int tile, count;               // its first slot and how many
+    int last;                      // the share ends with it
+    int c0, c1;                    // the CTAs that share the unit
 };
 
 __device__ __forceinline__ int load_acquire(const int* at) {
@@ -189,6 +211,7 @@ __device__ __forceinline__ int load_acquire(const int* at) {
 __device__ __forceinline__ void add_release(int* at) {
     asm volatile("red.release.cta.shared::cta.add.u32 [%0], 1;\n" ::"r"(smem_addr(at)) : "memory");
 }
+__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + exp2_fast(-x * kLog2e)); }
 
 // Raises the call's timeout flag and makes every role of the CTA leave at its next wait.
 __device__ __noinline__ void attn_abort(int32_t* err_flag, volatile int* stop) {
@@ -197,55 +220,57 @@ __device__ __noinline__ void attn_abort(int32_t* err_flag, volatile int* stop) {
 }
 
 template <int D, bool FP8, int WM>
-__global__ void __launch_bounds__(kAttnThreads, 1) attn_decode_kernel(const __grid_constant__ AttnArgs p) {
+__global__ void __launch_bounds__(kAttnThreads, 1)
+attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUtensorMap map_k,
+                   const __grid_constant__ CUtensorMap map_v, const int box) {
     using Gm = Geo<D, FP8, WM>;
-    constexpr int BM = Gm::BM, ST = Gm::ST, KS = Gm::KS, NG = Gm::NG, CPR = Gm::CPR, SLOTS = Gm::SLOTS, NQ = Gm::NQ;
-    constexpr int QB = Gm::QB, HALF = Gm::SLOTB / 2, ND = D / 8, CH = Gm::CH, JROW = Gm::JROW;
+    constexpr int BM = Gm::BM, ST = Gm::ST, KS = Gm::KS, NG = Gm::NG, CS = Gm::CS, CPR = Gm::CPR, SLOTS = Gm::SLOTS;
+    constexpr int NQ = Gm::NQ, QB = Gm::QB, QP = Gm::QP, HALF = Gm::HALF, ND = Gm::ND;
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char* ring = smem;
     unsigned char* qbuf = ring + SLOTS * Gm::SLOTB;
-    float* jbuf = reinterpret_cast<float*>(qbuf + NQ * QB);       // [2][8][16][JROW]
-    float* jm = jbuf + Gm::JOINB / 4;                             // [8][16] maxima of the computing warps
-    float* jl = jm + 8 * 16;                                      // [8][16] sums
-    float* qexp = jl + 8 * 16;                                    // [NQ][BM] (e4m3) power of two taken out of a query row
-    Unit* units = reinterpret_cast<Unit*>(qexp + NQ * BM);        // [NQ]
-    uint64_t* full = reinterpret_cast<uint64_t*>(units + 4);      // [SLOTS]
+    float4* jbuf = reinterpret_cast<float4*>(qbuf + NQ * QB);     // [4 warps][ND][32] joined accumulators
+    float* jm = reinterpret_cast<float*>(qbuf + NQ * QB + Gm::JOINB);  // [4][2][16] their maxima and sums
+    float* qexp = jm + 4 * 32;                                    // [NQ][BM] (e4m3) power of two taken out of a query row
+    Piece* pieces = reinterpret_cast<Piece*>(qexp + NQ * BM);     // [NQ], then the share's first and last split ones
+    uint64_t* full = reinterpret_cast<uint64_t*>(pieces + NQ + 2 + ((NQ + 2) & 1));  // [SLOTS]
     uint64_t* qfull = full + SLOTS;                               // [NQ]
     uint64_t* cbar = qfull + NQ;                                  // the computing warps' barrier
     // Releases are counted, not phased: a warp comes back to a place only every few turns, and
     // a barrier's phase parity cannot tell a turn from the one two before it.
     int* freed = reinterpret_cast<int*>(cbar + 1);                // [SLOTS] warps that are done with a slot, all turns
     int* qfreed = freed + SLOTS;                                  // [NQ] the same for a unit's queries
-    int* misc = qfreed + NQ;                 // [16] sums of the schedule's warps, 14: last, 15: stop
-    int* prefix = misc + 16;                                      // [B + 1] slots before each sequence
+    int* misc = qfreed + NQ;                                      // [16] sums of the schedule's warps; 12, 13: last to arrive; 15: stop
+    int* prefix = misc + 16;                                      // [B + 1] cost of the sequences before each
     volatile int* stop = misc + 15;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int Hkv = p.sh.Hkv, G = p.sh.G, ps = p.sh.page_size;
 
     if (tid == 0) {
         for (int i = 0; i < SLOTS; ++i) {
-            mbar_init(full + i, 32);
+            mbar_init(full + i, box ? 1 : 32);
             freed[i] = 0;
         }
         for (int i = 0; i < NQ; ++i) {
-            mbar_init(qfull + i, FP8 ? 32 : 64);
+            mbar_init(qfull + i, FP8 ? 32 : 1);
             qfreed[i] = 0;
         }
         mbar_init(cbar, kComputeWarps);
         *stop = 0;
         mbar_init_fence();
+        fence_proxy_async_smem();
     }
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
-    // ---- the schedule: slots of every sequence, summed ----
+    // ---- the schedule: the cost of every sequence, summed ----
     int total = 0;
     for (int base = 0; base < p.B; base += kAttnThreads) {
         const int b = base + tid;
         int t = 0;
         if (b < p.B) {
             const Seq s = load_seq<BM, ST>(p, b, blockIdx.x == 0);
-            t = s.tiles * s.row_tiles * Hkv;
+            if (s.tiles > 0) t = (s.tiles + kUnitCost) * s.row_tiles * Hkv;
         }
         int x = t;
 #pragma unroll
@@ -267,11 +292,31 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_decode_kernel(const __gr
     }
     if (tid == 0) prefix[p.B] = total;
     __syncthreads();
-    // as many CTAs as there are SMs, but no fewer slots a CTA than token groups
-    const int ctas = min((int)gridDim.x, (total + NG - 1) / NG);
+    // As many CTAs as there are SMs, but no fewer slots a CTA than token groups. CTA c has the
+    // places c * per + min(c, more) on: per of them, one more for the first ones. A unit takes
+    // kUnitCost places, which no slot stands for, and one for each slot.
+    const int ctas = min((int)gridDim.x, (total + NG + kUnitCost - 1) / (NG + kUnitCost));
     if ((int)blockIdx.x >= ctas) return;
-    const int share_lo = (int)((long)blockIdx.x * total / ctas);
-    const int share_n = (int)((long)(blockIdx.x + 1) * total / ctas) - share_lo;
+    const int per = total / ctas, more = total - per * ctas;
+    const int share_lo = blockIdx.x * per + min((int)blockIdx.x, more), share_hi = share_lo + per + ((int)blockIdx.x < more);
+    auto cta_of = [&](int place) {
+        const int big = more * (per + 1);
+        return place < big ? place / (per + 1) : more + (place - big) / per;
+    };
+    int b = 0;
+    {
+        int hi = p.B;
+        while (hi - b > 1) {
+            const int mid = (b + hi) >> 1;
+            if (prefix[mid] <= share_lo) b = mid; else hi = mid;
+        }
+    }
+    Seq s = load_seq<BM, ST>(p, b, false);  // the last sequence that starts at or before the share: it has units
+    int unit = (share_lo - prefix[b]) / (s.tiles + kUnitCost);  // row_tile * Hkv + kv head
+    int place = prefix[b] + unit * (s.tiles + kUnitCost) + kUnitCost;  // of the unit's first slot
+    int tile = max(share_lo - place, 0);
+    if (place + tile >= share_hi) return;  // nothing but a unit's overhead
+
     auto give_up = [&] { return *stop != 0; };
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (mbar_wait_deadline(bar, parity, kWaitTimeoutCycles, give_up)) return true;
@@ -294,147 +339,151 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_decode_kernel(const __gr
 
     if (warp >= kComputeWarps) {
         // ================= loading =================
-        if (D == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
         const int pw = warp - kComputeWarps;
-        if (pw >= share_n) return;
-        int b, unit, tile, ord = 0;
-        {
-            int lo = 0, hi = p.B;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (prefix[mid] <= share_lo) lo = mid; else hi = mid;
-            }
-            b = lo;  // the last sequence that starts at or before the share: it has slots
-        }
-        Seq s = load_seq<BM, ST>(p, b, false);
-        {
-            const int off = share_lo - prefix[b];
-            unit = off / s.tiles;
-            tile = off - unit * s.tiles;
-        }
-        // `by` slots on; counts the units passed
+        int ord = 0;
+        // `by` slots on; counts the units passed; false past the end of the share
         auto advance = [&](int by) {
             tile += by;
-            while (tile >= s.tiles) {
+            while (place + tile < share_hi && tile >= s.tiles) {
                 tile -= s.tiles;
+                place += s.tiles + kUnitCost;
                 ++ord;
-                if (++unit < s.row_tiles * Hkv) continue;
-                unit = 0;
-                do {
-                    ++b;
-                } while (prefix[b + 1] == prefix[b]);
-                s = load_seq<BM, ST>(p, b, false);
-            }
-        };
-        int tok[(ST + 31) / 32];  // this lane's token numbers (page * page_size + offset) of the slot, -1: none
-        auto find_tokens = [&] {
-#pragma unroll
-            for (int i = 0; i < (ST + 31) / 32; ++i) {
-                const int r = i * 32 + lane, pos = s.lo + tile * ST + r;
-                int t = -1;
-                if (r < ST && pos < s.past + s.n) {
-                    const int pg = pos / ps;
-                    const int page = __ldg(p.c.table + (size_t)s.slot * p.c.max_pages + pg);
-                    if (page >= 0 && page < p.c.num_pages) t = page * ps + (pos - pg * ps);
-                    else if (p.err_flag) atomicOr(p.err_flag, GDN_DEVICE_ERR_PAGE_BIT);
+                if (++unit == s.row_tiles * Hkv && place + tile < share_hi) {
+                    unit = 0;
+                    do {
+                        ++b;
+                    } while (prefix[b + 1] == prefix[b]);
+                    s = load_seq<BM, ST>(p, b, false);
                 }
-                tok[i] = t;
             }
+            return place + tile < share_hi;
         };
         const size_t token_stride = (size_t)Hkv * Gm::ROWB;
+        // With TMA, lane x (16 + x) fetches chunk x of the slot's keys (values), `box` tokens of
+        // one page; otherwise a lane looks tokens up for everybody.
+        constexpr int LOOK = (ST + 31) / 32;
+        int tok[LOOK];  // token numbers (page * page_size + offset), -1: none
+        auto look_up = [&](int pos, int len) {
+            if (pos + len <= s.lo || pos >= s.past + s.n) return -1;
+            const int pg = pos / ps;
+            const int page = __ldg(p.c.table + (size_t)s.slot * p.c.max_pages + pg);
+            if (page >= 0 && page < p.c.num_pages) return page * ps + (pos - pg * ps);
+            if (p.err_flag) atomicOr(p.err_flag, GDN_DEVICE_ERR_PAGE_BIT);
+            return -1;
+        };
+        auto find_tokens = [&] {
+            const int pos0 = s.base + tile * ST;
+            if (box) {
+                const int x = lane & 15;
+                tok[0] = x * box < ST ? look_up(pos0 + x * box, box) : -1;
+            } else {
+#pragma unroll
+                for (int i = 0; i < LOOK; ++i) tok[i] = i * 32 + lane < ST ? look_up(pos0 + i * 32 + lane, 1) : -1;
+            }
+        };
         constexpr int RPP = 32 / CPR;  // token rows of one warp-wide copy
         const int chunk = lane % CPR, sub = lane / CPR;
-        if (pw > 0) advance(pw);
-        find_tokens();
-        for (int i = pw; i < share_n; i += kLoadWarps) {
-            const int h = unit % Hkv, rt = unit / Hkv;
+        bool more_slots = pw == 0 || advance(pw);
+        if (more_slots) find_tokens();
+        for (int i = pw; more_slots; i += kLoadWarps) {
+            const int rt = unit / Hkv, h = unit - rt * Hkv;
             const int st = i % SLOTS, turn = i / SLOTS;
-            if (i == 0 || tile == 0) {
-                // the unit's queries: row r is token r / G, query head h * G + r % G
-                const int qs = ord % NQ, qturn = ord / NQ;
-                if (!wait_count(qfreed + qs, qturn * kComputeWarps)) break;
-                if (lane == 0) {
-                    Unit u;
-                    u.s = s;
-                    u.h = h;
-                    u.rt = rt;
-                    u.tile = tile;
-                    u.count = min(s.tiles - tile, share_n - i);
-                    u.lo = prefix[b] + unit * s.tiles;
-                    units[qs] = u;
-                }
-                const int rows = s.n * G;
-                unsigned char* q = qbuf + qs * QB;
-                if (!FP8) {
-                    for (int k = lane; k < BM * (D / 8); k += 32) {
-                        const int r = k / (D / 8), c = k % (D / 8), rr = rt * BM + r, t = rr / G;
-                        const uint16_t* src = p.q.ptr;
-                        if (rr < rows) src += (size_t)(s.first + t) * p.q.row + (size_t)(h * G + rr - t * G) * p.q.head + c * 8;
-                        cp16(smem_addr(q + (r * (D / 8) + (c ^ (r & 7))) * 16), src, rr < rows);
+            if (!wait_count(freed + st, turn * Gm::READERS)) break;
+            const uint32_t at = smem_addr(ring + st * Gm::SLOTB);
+            if (box) {
+                const unsigned got = __ballot_sync(0xffffffffu, tok[0] >= 0);
+                if (lane == 0) mbar_arrive_expect_tx(full + st, __popc(got) * box * Gm::ROWB);
+                __syncwarp();
+                if (tok[0] >= 0)
+                    tma_load_5d(at + (lane >> 4) * HALF + (lane & 15) * box * Gm::ROWB, lane < 16 ? &map_k : &map_v, tok[0] >> 3, h,
+                                smem_addr(full + st));
+            } else {
+                const unsigned char* kb = static_cast<const unsigned char*>(p.c.k) + (size_t)h * Gm::ROWB + chunk * 16;
+                const unsigned char* vb = static_cast<const unsigned char*>(p.c.v) + (size_t)h * Gm::ROWB + chunk * 16;
+#pragma unroll 1
+                for (int k = 0; k < ST / RPP; k += 8) {
+                    int t[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        const int r = (k + x) * RPP;
+                        int v = tok[0];
+#pragma unroll
+                        for (int y = 1; y < LOOK; ++y) v = (r >> 5) == y ? tok[y] : v;
+                        t[x] = __shfl_sync(0xffffffffu, v, (r + sub) & 31);
                     }
-                    cp_async_arrive(qfull + qs);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        const size_t off = t[x] < 0 ? 0 : (size_t)t[x] * token_stride;
+                        const uint32_t to = at + chunk_at<CPR>((k + x) * RPP + sub, chunk);
+                        cp16(to, kb + off, t[x] >= 0);
+                        cp16(to + HALF, vb + off, t[x] >= 0);
+                    }
+                }
+                cp_async_arrive(full + st);
+            }
+            if (i == 0 || tile == 0) {
+                // the unit's queries: row r is token r / G, query head h * G + r % G; rows past the last
+                // are left as they are (a row's products touch no other row)
+                const int qs = ord % NQ, rows = min(BM, s.n * G - rt * BM);
+                const int inv_g = 65536 / G + 1;  // r / G = r * inv_g >> 16 for r < 320, G <= 16
+                if (!wait_count(qfreed + qs, ord / NQ * kComputeWarps)) break;
+                unsigned char* q = qbuf + qs * QB;
+                if (lane == 0) {
+                    const int count = min(s.tiles - tile, share_hi - place - tile);
+                    const int next = tile + count == s.tiles ? place + s.tiles + kUnitCost : share_hi;
+                    pieces[qs] = Piece{s.n, s.first, s.past, s.lo, s.base, h, rt, tile, count, next >= share_hi,
+                                       cta_of(place), cta_of(place + s.tiles - 1)};
+                    if (!FP8) mbar_arrive_expect_tx(qfull + qs, rows * D * 2);
+                }
+                __syncwarp();
+                auto row_of = [&](int r) {
+                    const int rr = rt * BM + r, t = (rr * inv_g) >> 16;
+                    return p.q.ptr + (size_t)(s.first + t) * p.q.row + (size_t)(h * G + rr - t * G) * p.q.head;
+                };
+                if (!FP8) {
+                    for (int r = lane; r < rows; r += 32) tma_load_1d(q + r * QP, row_of(r), D * 2, qfull + qs);
                 } else {
                     // e4m3 keys become fp16, so the queries do too: a power of two per row brings its
                     // largest element to 2^14 .. 2^15, exact for every element above 2^-38 of that
-#pragma unroll 2
-                    for (int r = 0; r < BM; ++r) {
-                        const int rr = rt * BM + r, t = rr / G;
-                        const uint32_t* src = reinterpret_cast<const uint32_t*>(
-                            p.q.ptr + (size_t)(s.first + t) * p.q.row + (size_t)(h * G + rr - t * G) * p.q.head);
-                        uint32_t w[D / 64], top = 0;
+                    constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes a row, rows at a time
+#pragma unroll 4
+                    for (int r0 = 0; r0 < BM; r0 += RPW) {
+                        const int r = r0 + lane / LPR, c = lane % LPR;
+                        const uint4 w = r < rows ? __ldg(reinterpret_cast<const uint4*>(row_of(r)) + c) : make_uint4(0, 0, 0, 0);
+                        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+                        uint32_t top = 0;
 #pragma unroll
-                        for (int k = 0; k < D / 64; ++k) {
-                            w[k] = rr < rows ? __ldg(src + lane + 32 * k) : 0;
-                            top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
-                        }
-                        top = __reduce_max_sync(0xffffffffu, top);
+                        for (int k = 0; k < 4; ++k) top = max(top, max(v[k] & 0x7fffu, (v[k] >> 16) & 0x7fffu));
+#pragma unroll
+                        for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
                         const int e = top == 0 || top >= 0x7f80u ? 0 : max((int)(top >> 7), 1) - 127 - 14;
-                        const float up = ldexpf(1.0f, -e);
+                        // 2^-e: e is at most 113, and at least -140, where the exponent field ends
+                        const float up = __uint_as_float((uint32_t)(127 - max(e, -127)) << 23);
+                        uint32_t z[4];
 #pragma unroll
-                        for (int k = 0; k < D / 64; ++k) {
-                            const int x = lane + 32 * k;  // pair of elements; four pairs a chunk
-                            *reinterpret_cast<uint32_t*>(q + (r * (D / 8) + ((x >> 2) ^ (r & 7))) * 16 + (x & 3) * 4) =
-                                pack2<true>(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xffff0000u) * up);
-                        }
-                        if (lane == 0) qexp[qs * BM + r] = ldexpf(1.0f, e);
+                        for (int k = 0; k < 4; ++k) z[k] = pack2<true>(__uint_as_float(v[k] << 16) * up, __uint_as_float(v[k] & 0xffff0000u) * up);
+                        *reinterpret_cast<uint4*>(q + r * QP + c * 16) = make_uint4(z[0], z[1], z[2], z[3]);
+                        if (c == 0) qexp[qs * BM + r] = 1.0f / up;
                     }
+                    mbar_arrive(qfull + qs);
                 }
-                mbar_arrive(qfull + qs);
             }
-            if (!wait_count(freed + st, turn * WM)) break;
-            const uint32_t at = smem_addr(ring + st * Gm::SLOTB);
-            const unsigned char* kb = static_cast<const unsigned char*>(p.c.k) + (size_t)h * Gm::ROWB + chunk * 16;
-            const unsigned char* vb = static_cast<const unsigned char*>(p.c.v) + (size_t)h * Gm::ROWB + chunk * 16;
-#pragma unroll
-            for (int k = 0; k < ST / RPP; ++k) {
-                const int r = k * RPP + sub;
-                const int t = __shfl_sync(0xffffffffu, tok[(k * RPP) / 32], r & 31);
-                const size_t off = t < 0 ? 0 : (size_t)t * token_stride;
-                const uint32_t to = at + chunk_at<CPR>(r, chunk);
-                cp16(to, kb + off, t >= 0);
-                cp16(to + HALF, vb + off, t >= 0);
-            }
-            cp_async_arrive(full + st);
-            if (i + kLoadWarps < share_n) {
-                advance(kLoadWarps);
-                find_tokens();
-            }
+            more_slots = advance(kLoadWarps);
+            if (more_slots) find_tokens();
         }
-        cp_commit();
-        cp_wait<0>();
+        cp_wait_all();
         return;
     }
 
     // ================= computing =================
-    if (D == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;\n");
-    const int wm = warp % WM, grp = warp / WM;
+    const int wm = warp % WM, cs = warp / WM % CS, grp = warp / (WM * CS);
     const int g = lane >> 2, j = lane & 3;
     const bool capped = p.sh.softcap > 0.0f;
     const float qk_scale = p.sh.sm_scale * p.sh.k_scale;
     const float to_log2 = capped ? p.sh.softcap * kLog2e : qk_scale * kLog2e;  // after the cap, or at once
     const float cap_in = capped ? 2.0f * kLog2e * qk_scale / p.sh.softcap : 0.0f;
     uint32_t cphase = 0;
-    // all computing warps; what they wrote to shared memory before is visible after it
+    // all computing warps; what they wrote before is visible to them after it
     auto meet = [&]() -> bool {
         __syncwarp();
         if (lane == 0) mbar_arrive(cbar);
@@ -442,20 +491,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_decode_kernel(const __gr
         cphase ^= 1;
         return ok;
     };
+    constexpr int PSTRIDE = BM * (D + 2);  // floats of a partial result: [BM][D], then maxima and sums
+    bool split_first = false, split_last = false;
 
-    for (int done = 0, ord = 0; done < share_n; ++ord) {
+    bool last = false;
+    for (int done = 0, ord = 0; !last; ++ord) {
         const int qs = ord % NQ;
         if (!wait(qfull + qs, (ord / NQ) & 1)) return;
-        const Unit u = units[qs];
-        const uint32_t qaddr = smem_addr(qbuf + qs * QB);
+        const Piece u = pieces[qs];
+        last = u.last != 0;
+        uint32_t qaddr = smem_addr(qbuf + qs * QB);
+        after_wait(qaddr);
         const unsigned char* qrow = qbuf + qs * QB;
-        const int kv_len = u.s.past + u.s.n;
+        const int kv_len = u.past + u.n;
         // row r attends positions lo .. hi-1; every row of the unit those from all_lo to all_hi
         const int r0 = u.rt * BM + wm * 16 + g, t0 = r0 / G, t1 = (r0 + 8) / G;
-        const int hi0 = min(u.s.past + t0 + 1, kv_len), hi1 = min(u.s.past + t1 + 1, kv_len);
-        const int lo0 = p.sh.window > 0 ? u.s.past + t0 + 1 - p.sh.window : 0;
-        const int lo1 = p.sh.window > 0 ? u.s.past + t1 + 1 - p.sh.window : 0;
-        const int all_lo = p.sh.window > 0 ? max(0, kv_len - p.sh.window) : 0, all_hi = u.s.past + 1;
+        const int hi0 = min(u.past + t0 + 1, kv_len), hi1 = min(u.past + t1 + 1, kv_len);
+        const int lo0 = p.sh.window > 0 ? u.past + t0 + 1 - p.sh.window : 0;
+        const int lo1 = p.sh.window > 0 ? u.past + t1 + 1 - p.sh.window : 0;
+        const int all_lo = p.sh.window > 0 ? max(0, kv_len - p.sh.window) : 0, all_hi = u.past + 1;
         float e0 = 1.0f, e1 = 1.0f;
         if (FP8) {
             e0 = qexp[qs * BM + wm * 16 + g];
@@ -466,14 +520,29 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_decode_kernel(const __gr
         for (int i = 0; i < ND; ++i) O[i][0] = O[i][1] = O[i][2] = O[i][3] = 0.0f;
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};  // rows g, g + 8: maximum (log2 units), sum
 
-        // this group's slots of the piece: those whose number in the share is grp modulo NG
-        for (int i = (grp - done % NG + NG) % NG; i < u.count; i += NG) {
+        // this group's slots: all of a short piece, in turn with the other groups, or every NG-th
+        const bool single = NG == 1 || u.count <= kSingle;
+        const int owner = single ? ord % NG : 0;
+        for (int i = single ? (grp == owner ? 0 : u.count) : (grp + NG - done % NG) % NG; i < u.count; i += single ? 1 : NG) {
             const int n = done + i, st = n % SLOTS, turn = n / SLOTS;
             // the turn before is over (it may be another group's), so the parity is this turn's
-            if (!wait_count(freed + st, turn * WM) || !wait(full + st, turn & 1)) return;
-            const unsigned char* kt = ring + st * Gm::SLOTB;
-            const uint32_t ks = smem_addr(kt), vs = ks + HALF;
-            const int pos0 = u.s.lo + (u.tile + i) * ST;
+            if (!wait_count(freed + st, turn * Gm::READERS) || !wait(full + st, turn & 1)) return;
+            unsigned char* kt = ring + st * Gm::SLOTB;
+            uint32_t ks = smem_addr(kt);
+            after_wait(ks);
+            const uint32_t vs = ks + HALF;
+            const int pos0 = u.base + (u.tile + i) * ST;
+            const bool whole = pos0 >= all_lo && pos0 + ST <= all_hi;
+            if (pos0 < u.lo || pos0 + ST > kv_len) {
+                // values of places outside the sequence become zeros
+                for (int x = lane; x < ST * CPR; x += 32) {
+                    const int r = x / CPR;
+                    if (pos0 + r < u.lo || pos0 + r >= kv_len)
+                        *reinterpret_cast<uint4*>(kt + HALF + chunk_at<CPR>(r, x % CPR)) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();  // before the slot is filled again
+                __syncwarp();
+            }
             float S[KS * 2][4];
 #pragma unroll
             for (int x = 0; x < KS * 2; ++x) S[x][0] = S[x][1] = S[x][2] = S[x][3] = 0.0f;
@@ -481,15 +550,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_decode_kernel(const __gr
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     uint32_t a[4];
-                    const int qr = wm * 16 + (lane & 15), qc = kk * 2 + (lane >> 4);
-                    ldsm4(a, qaddr + (qr * (D / 8) + (qc ^ (qr & 7))) * 16);
+                    ldsm4(a, qaddr + (wm * 16 + (lane & 15)) * QP + (kk * 2 + (lane >> 4)) * 16);
 #pragma unroll
-                    for (int s = 0; s < KS; ++s) {
-                        uint32_t b[4];
-                        const int r = s * 16 + (lane & 7) + ((lane >> 4) << 3), c = kk * 2 + ((lane >> 3) & 1);
-                        ldsm4(b, ks + chunk_at<CPR>(r, c));
-                        mma<false>(S[2 * s], a, b[0], b[1]);
-                        mma<false>(S[2 * s + 1], a, b[2], b[3]);
+                    for (int x = 0; x < KS; ++x) {
+                        uint32_t v[4];
+                        ldsm4(v, ks + chunk_at<CPR>(x * 16 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)));
+                        mma<false>(S[2 * x], a, v[0], v[1]);
+                        mma<false>(S[2 * x + 1], a, v[2], v[3]);
                     }
                 }
             } else {
@@ -500,27 +567,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_decode_kernel(const __gr
                     uint32_t a[2][4];
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const int c = (kk + x) * 2 + (j >> 1), ra = wm * 16 + g, rb = ra + 8;
-                        const uint2 q0 = *reinterpret_cast<const uint2*>(qrow + (ra * (D / 8) + (c ^ (ra & 7))) * 16 + (j & 1) * 8);
-                        const uint2 q1 = *reinterpret_cast<const uint2*>(qrow + (rb * (D / 8) + (c ^ (rb & 7))) * 16 + (j & 1) * 8);
+                        const uint2 q0 = *reinterpret_cast<const uint2*>(qrow + (wm * 16 + g) * QP + (kk + x) * 32 + j * 8);
+                        const uint2 q1 = *reinterpret_cast<const uint2*>(qrow + (wm * 16 + g + 8) * QP + (kk + x) * 32 + j * 8);
                         a[x][0] = q0.x;
                         a[x][1] = q1.x;
                         a[x][2] = q0.y;
                         a[x][3] = q1.y;
                     }
 #pragma unroll
-                    for (int s = 0; s < KS; ++s) {
-                        uint32_t b[4];  // tokens 0-7 and 8-15 of chunk kk, then of chunk kk + 1
-                        ldsm4(b, ks + chunk_at<CPR>(s * 16 + (lane & 15), kk + (lane >> 4)));
+                    for (int y = 0; y < KS; ++y) {
+                        uint32_t v[4];  // tokens 0-7 and 8-15 of chunk kk, then of chunk kk + 1
+                        ldsm4(v, ks + chunk_at<CPR>(y * 16 + (lane & 15), kk + (lane >> 4)));
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            mma<true>(S[2 * s], a[x], e4m3_to_half2(b[2 * x], false), e4m3_to_half2(b[2 * x], true));
-                            mma<true>(S[2 * s + 1], a[x], e4m3_to_half2(b[2 * x + 1], false), e4m3_to_half2(b[2 * x + 1], true));
+                            mma<true>(S[2 * y], a[x], e4m3_to_half2(v[2 * x], false), e4m3_to_half2(v[2 * x], true));
+                            mma<true>(S[2 * y + 1], a[x], e4m3_to_half2(v[2 * x + 1], false), e4m3_to_half2(v[2 * x + 1], true));
                         }
                     }
                 }
             }
-            const bool whole = pos0 >= all_lo && pos0 + ST <= all_hi;
             float mx0 = m[0], mx1 = m[1];
 #pragma unroll
             for (int x = 0; x < KS * 2; ++x) {
@@ -584,31 +649,31 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_decode_kernel(const __gr
             }
             if (plain) {
 #pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    const uint32_t a[4] = {pack2<FP8>(S[2 * s][0], S[2 * s][1]), pack2<FP8>(S[2 * s][2], S[2 * s][3]),
-                                           pack2<FP8>(S[2 * s + 1][0], S[2 * s + 1][1]), pack2<FP8>(S[2 * s + 1][2], S[2 * s + 1][3])};
-                    const int r = s * 16 + (lane & 15);
+                for (int x = 0; x < KS; ++x) {
+                    const uint32_t a[4] = {pack2<FP8>(S[2 * x][0], S[2 * x][1]), pack2<FP8>(S[2 * x][2], S[2 * x][3]),
+                                           pack2<FP8>(S[2 * x + 1][0], S[2 * x + 1][1]), pack2<FP8>(S[2 * x + 1][2], S[2 * x + 1][3])};
+                    const int r = x * 16 + (lane & 15);
                     if (!FP8) {
 #pragma unroll
-                        for (int c = 0; c < D / 16; ++c) {
-                            uint32_t b[4];
-                            ldsm4t(b, vs + chunk_at<CPR>(r, c * 2 + (lane >> 4)));
-                            mma<false>(O[2 * c], a, b[0], b[1]);
-                            mma<false>(O[2 * c + 1], a, b[2], b[3]);
+                        for (int c = 0; c < ND / 2; ++c) {
+                            uint32_t v[4];
+                            ldsm4t(v, vs + chunk_at<CPR>(r, cs * ND + c * 2 + (lane >> 4)));
+                            mma<false>(O[2 * c], a, v[0], v[1]);
+                            mma<false>(O[2 * c + 1], a, v[2], v[3]);
                         }
                     } else {
                         // a transposed pair of bytes is columns 2n, 2n+1 of one token: tile 2c takes the
                         // even columns of chunk c, tile 2c + 1 the odd ones
 #pragma unroll
-                        for (int c = 0; c < D / 16; c += 2) {
-                            uint32_t b[4];
-                            ldsm4t(b, vs + chunk_at<CPR>(r, c + (lane >> 4)));
+                        for (int c = 0; c < ND / 2; c += 2) {
+                            uint32_t v[4];
+                            ldsm4t(v, vs + chunk_at<CPR>(r, cs * (ND / 2) + c + (lane >> 4)));
 #pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const uint32_t x0 = e4m3_to_half2(b[2 * x], false), y0 = e4m3_to_half2(b[2 * x], true);
-                                const uint32_t x1 = e4m3_to_half2(b[2 * x + 1], false), y1 = e4m3_to_half2(b[2 * x + 1], true);
-                                mma<true>(O[2 * (c + x)], a, __byte_perm(x0, y0, 0x5410), __byte_perm(x1, y1, 0x5410));
-                                mma<true>(O[2 * (c + x) + 1], a, __byte_perm(x0, y0, 0x7632), __byte_perm(x1, y1, 0x7632));
+                            for (int y = 0; y < 2; ++y) {
+                                const uint32_t x0 = e4m3_to_half2(v[2 * y], false), y0 = e4m3_to_half2(v[2 * y], true);
+                                const uint32_t x1 = e4m3_to_half2(v[2 * y + 1], false), y1 = e4m3_to_half2(v[2 * y + 1], true);
+                                mma<true>(O[2 * (c + y)], a, __byte_perm(x0, y0, 0x5410), __byte_perm(x1, y1, 0x5410));
+                                mma<true>(O[2 * (c + y) + 1], a, __byte_perm(x0, y0, 0x7632), __byte_perm(x1, y1, 0x7632));
                             }
                         }
                     }
@@ -634,10 +699,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_decode_kernel(const __gr
                         for (int e = 0; e < 2; ++e) {
                             float v;
                             if (!FP8) {
-                                const int col = x * 8 + 2 * j + e;
+                                const int col = cs * (ND * 8) + x * 8 + 2 * j + e;
                                 v = bf16_bits_to_float(*reinterpret_cast<const uint16_t*>(kt + HALF + chunk_at<CPR>(t, col >> 3) + (col & 7) * 2));
                             } else {
-                                const int col = (x >> 1) * 16 + 4 * j + 2 * e + (x & 1);
+                                const int col = cs * (ND * 8) + (x >> 1) * 16 + 4 * j + 2 * e + (x & 1);
                                 const uint32_t hh = e4m3_to_half2(*(kt + HALF + chunk_at<CPR>(t, col >> 4) + (col & 15)), false);
                                 v = __low2float(*reinterpret_cast<const __half2*>(&hh));
                             }
@@ -647,189 +712,231 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_decode_kernel(const __gr
                     }
                 }
             }
+            before_release(O);
             __syncwarp();
             if (lane == 0) add_release(freed + st);
         }
         done += u.count;
         __syncwarp();
         if (lane == 0) add_release(qfreed + qs);
-
-        // ---- the piece's token groups joined: a common maximum, then CH columns at a time ----
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
         }
-        // (the last readers of jm and jl left their previous use at a later barrier than this one's arrival)
-        if (j == 0) {
-            jm[warp * 16 + g] = m[0];
-            jm[warp * 16 + g + 8] = m[1];
-            jl[warp * 16 + g] = l[0];
-            jl[warp * 16 + g + 8] = l[1];
-        }
-        if (!meet()) return;
-        auto top_of = [&](int w, int r) {  // row r of row group w
-            float x = jm[w * 16 + r];
+
+        // ---- the token groups joined, half of them into the other half, down to group 0 ----
+        if (NG > 1 && !single) {
+            if (!meet()) return;  // the last join's reads are done
 #pragma unroll
-            for (int k = 1; k < NG; ++k) x = fmaxf(x, jm[(k * WM + w) * 16 + r]);
-            return x;
-        };
-        {
-            const float a = top_of(wm, g), b = top_of(wm, g + 8);
-            const float f0 = m[0] == -INFINITY ? 0.0f : exp2_fast(m[0] - a), f1 = m[1] == -INFINITY ? 0.0f : exp2_fast(m[1] - b);
+            for (int half = NG / 2; half >= 1; half >>= 1) {
+                // a group writes where it was the last to read: region (reader) + NG / 2 - half
+                const int region = ((grp % half) + NG / 2 - half) * Gm::READERS + warp % Gm::READERS;
+                float4* at = jbuf + region * ND * 32 + lane;
+                float* jr = jm + region * 32;
+                if (grp >= half && grp < 2 * half) {
 #pragma unroll
-            for (int x = 0; x < ND; ++x) {
-                O[x][0] *= f0;
-                O[x][1] *= f0;
-                O[x][2] *= f1;
-                O[x][3] *= f1;
+                    for (int x = 0; x < ND; ++x) at[x * 32] = make_float4(O[x][0], O[x][1], O[x][2], O[x][3]);
+                    if (j == 0) {
+                        jr[g] = m[0];
+                        jr[g + 8] = m[1];
+                        jr[16 + g] = l[0];
+                        jr[24 + g] = l[1];
+                    }
+                }
+                if (!meet()) return;
+                if (grp < half) {
+                    const float om0 = jr[g], om1 = jr[g + 8];
+                    const float n0 = fmaxf(m[0], om0), n1 = fmaxf(m[1], om1);
+                    const float z0 = n0 == -INFINITY ? 0.0f : n0, z1 = n1 == -INFINITY ? 0.0f : n1;
+                    const float a0 = exp2_fast(m[0] - z0), a1 = exp2_fast(m[1] - z1);
+                    const float b0 = exp2_fast(om0 - z0), b1 = exp2_fast(om1 - z1);
+                    l[0] = l[0] * a0 + jr[16 + g] * b0;
+                    l[1] = l[1] * a1 + jr[24 + g] * b1;
+                    m[0] = n0;
+                    m[1] = n1;
+#pragma unroll
+                    for (int x = 0; x < ND; ++x) {
+                        const float4 o = at[x * 32];
+                        O[x][0] = O[x][0] * a0 + o.x * b0;
+                        O[x][1] = O[x][1] * a0 + o.y * b0;
+                        O[x][2] = O[x][2] * a1 + o.z * b1;
+                        O[x][3] = O[x][3] * a1 + o.w * b1;
+                    }
+                }
             }
         }
-        const int unit_hi = u.lo + u.s.tiles;
-        const int c0 = (int)(((long)(u.lo + 1) * ctas - 1) / total), c1 = (int)(((long)unit_hi * ctas - 1) / total);
-        const bool split = c0 != c1;
-        const int rows = min(BM, u.s.n * G - u.rt * BM);
-        constexpr int PSTRIDE = BM * (D + 2);  // floats of a partial result: [BM][D], then maxima and sums
-        float* mine = p.partial + (size_t)(blockIdx.x * 2 + (split && (int)blockIdx.x != c0 && share_lo > u.lo ? 0 : 1)) * PSTRIDE;
-        auto gate_of = [&](int r, int col) -> uint2 {
+
+        // ---- the owner's warps write the result, or the piece of it (fp32, unnormalised) ----
+        const bool split = u.c0 != u.c1;
+        const int rows = min(BM, u.n * G - u.rt * BM);
+        if (split) {
+            // the first CTA's piece ends its share, the others' begin theirs
+            const int which = (int)blockIdx.x == u.c0;
+            if (which) split_last = true; else split_first = true;
+            if (warp == 0 && lane == 0) pieces[NQ + which] = u;
+        }
+        if (grp == owner) {
+            const int a = wm * 16 + g;
+            const bool in0 = a < rows, in1 = a + 8 < rows;
+            if (split) {
+                float* mine = p.partial + (size_t)(blockIdx.x * 2 + ((int)blockIdx.x == u.c0)) * PSTRIDE;
+#pragma unroll
+                for (int x = 0; x < ND; x += 2) {
+                    const int col = cs * (ND * 8) + x * 8;
+                    if (!FP8) {
+                        if (in0) {
+                            *reinterpret_cast<float2*>(mine + a * D + col + 2 * j) = make_float2(O[x][0], O[x][1]);
+                            *reinterpret_cast<float2*>(mine + a * D + col + 8 + 2 * j) = make_float2(O[x + 1][0], O[x + 1][1]);
+                        }
+                        if (in1) {
+                            *reinterpret_cast<float2*>(mine + (a + 8) * D + col + 2 * j) = make_float2(O[x][2], O[x][3]);
+                            *reinterpret_cast<float2*>(mine + (a + 8) * D + col + 8 + 2 * j) = make_float2(O[x + 1][2], O[x + 1][3]);
+                        }
+                    } else {
+                        if (in0) *reinterpret_cast<float4*>(mine + a * D + col + 4 * j) = make_float4(O[x][0], O[x + 1][0], O[x][1], O[x + 1][1]);
+                        if (in1) *reinterpret_cast<float4*>(mine + (a + 8) * D + col + 4 * j) = make_float4(O[x][2], O[x + 1][2], O[x][3], O[x + 1][3]);
+                    }
+                }
+                if (j == 0 && cs == 0) {
+                    mine[BM * D + a] = m[0];
+                    mine[BM * D + a + 8] = m[1];
+                    mine[BM * D + BM + a] = l[0];
+                    mine[BM * D + BM + a + 8] = l[1];
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (!(e ? in1 : in0)) continue;
+                    const int t = e ? t1 : t0, head = u.h * G + (r0 + 8 * e) - t * G;
+                    const size_t row = (size_t)u.first + t, at = row * p.sh.Hq + head;
+                    uint16_t* out = p.out + at * D + cs * (ND * 8);
+                    const uint16_t* gate = p.gate.ptr + row * p.gate.row + (size_t)head * p.gate.head + cs * (ND * 8);
+                    const float inv = p.sh.v_scale / l[e];
+                    if (!FP8) {
+                        uint32_t z[ND];
+                        if (p.gate.ptr) {
+#pragma unroll
+                            for (int x = 0; x < ND; ++x) z[x] = __ldg(reinterpret_cast<const uint32_t*>(gate + x * 8 + 2 * j));
+                        }
+#pragma unroll
+                        for (int x = 0; x < ND; ++x) {
+                            float v0 = O[x][2 * e] * inv, v1 = O[x][2 * e + 1] * inv;
+                            if (p.gate.ptr) {
+                                v0 *= sigmoid_fast(__uint_as_float(z[x] << 16));
+                                v1 *= sigmoid_fast(__uint_as_float(z[x] & 0xffff0000u));
+                            }
+                            *reinterpret_cast<uint32_t*>(out + x * 8 + 2 * j) = pack2<false>(v0, v1);
+                        }
+                    } else {
+                        uint2 z[ND / 2];
+                        if (p.gate.ptr) {
+#pragma unroll
+                            for (int x = 0; x < ND / 2; ++x) z[x] = __ldg(reinterpret_cast<const uint2*>(gate + x * 16 + 4 * j));
+                        }
+#pragma unroll
+                        for (int x = 0; x < ND / 2; ++x) {
+                            float v0 = O[2 * x][2 * e] * inv, v1 = O[2 * x + 1][2 * e] * inv, v2 = O[2 * x][2 * e + 1] * inv, v3 = O[2 * x + 1][2 * e + 1] * inv;
+                            if (p.gate.ptr) {
+                                v0 *= sigmoid_fast(__uint_as_float(z[x].x << 16));
+                                v1 *= sigmoid_fast(__uint_as_float(z[x].x & 0xffff0000u));
+                                v2 *= sigmoid_fast(__uint_as_float(z[x].y << 16));
+                                v3 *= sigmoid_fast(__uint_as_float(z[x].y & 0xffff0000u));
+                            }
+                            *reinterpret_cast<uint2*>(out + x * 16 + 4 * j) = make_uint2(pack2<false>(v0, v1), pack2<false>(v2, v3));
+                        }
+                    }
+                    if (p.lse && cs == 0 && j == 0) p.lse[at] = (m[e] + log2f(l[e])) * kLn2;
+                }
+            }
+        }
+    }
+
+    // ---- units over several CTAs: the last of them to get here joins the pieces, in their order ----
+    if (!split_first && !split_last) return;
+    __threadfence();
+    if (!meet()) return;
+    if (tid < 2 && (tid == 0 ? split_first : split_last)) {
+        const Piece& u = pieces[NQ + tid];
+        misc[12 + tid] = atomicAdd(p.counters + u.c0, 1u) == (unsigned)(u.c1 - u.c0);
+    }
+    if (!meet()) return;
+    for (int which = 0; which < 2; ++which) {
+        if (!(which ? split_last : split_first) || !misc[12 + which]) continue;
+        __threadfence();
+        const Piece u = pieces[NQ + which];
+        const int rows = min(BM, u.n * G - u.rt * BM), count = u.c1 - u.c0 + 1;
+        auto part = [&](int i) -> const float* { return p.partial + (size_t)((u.c0 + i) * 2 + (i == 0)) * PSTRIDE; };
+        float* wt = reinterpret_cast<float*>(ring);  // [BM][kAttnMaxCtas + 2] weights of the pieces, their sum and maximum
+        constexpr int WP = kAttnMaxCtas + 2;
+        static_assert(BM * WP * 4 <= SLOTS * Gm::SLOTB, "weights");
+        if (!meet()) return;
+        for (int r = warp; r < rows; r += kComputeWarps) {
+            float* w = wt + r * WP;
+            float top = -INFINITY, tot = 0.0f;
+            for (int i = lane; i < count; i += 32) {
+                w[i] = __ldcg(part(i) + BM * D + r);
+                top = fmaxf(top, w[i]);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            for (int i = lane; i < count; i += 32) {
+                w[i] = w[i] == -INFINITY ? 0.0f : exp2_fast(w[i] - top);
+                tot = fmaf(w[i], __ldcg(part(i) + BM * D + BM + r), tot);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+            if (lane == 0) {
+                w[kAttnMaxCtas] = tot;
+                w[kAttnMaxCtas + 1] = top;
+            }
+        }
+        if (!meet()) return;
+        for (int k = tid; k < rows * (D / 4); k += kComputeWarps * 32) {
+            const int r = k / (D / 4), col = (k % (D / 4)) * 4;
+            const float* w = wt + r * WP;
             const int rr = u.rt * BM + r, t = rr / G, head = u.h * G + rr - t * G;
-            return __ldg(reinterpret_cast<const uint2*>(p.gate.ptr + (size_t)(u.s.first + t) * p.gate.row + (size_t)head * p.gate.head + col));
-        };
-        auto finish = [&](int r, int col, float4 o, float mx, float sum, uint2 w) {  // four normalised columns of row r
-            const int rr = u.rt * BM + r, t = rr / G, head = u.h * G + rr - t * G;
-            const size_t at = (size_t)(u.s.first + t) * p.sh.Hq + head;
+            const size_t row = (size_t)u.first + t, at = row * p.sh.Hq + head;
+            uint2 z = make_uint2(0, 0);
+            if (p.gate.ptr) z = __ldg(reinterpret_cast<const uint2*>(p.gate.ptr + row * p.gate.row + (size_t)head * p.gate.head + col));
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+            for (int i = 0; i < count; ++i) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(part(i) + r * D + col));
+                o.x = fmaf(w[i], x.x, o.x);
+                o.y = fmaf(w[i], x.y, o.y);
+                o.z = fmaf(w[i], x.z, o.z);
+                o.w = fmaf(w[i], x.w, o.w);
+            }
+            const float inv = p.sh.v_scale / w[kAttnMaxCtas];
+            o.x *= inv;
+            o.y *= inv;
+            o.z *= inv;
+            o.w *= inv;
             if (p.gate.ptr) {
-                o.x *= sigmoid(__uint_as_float(w.x << 16));
-                o.y *= sigmoid(__uint_as_float(w.x & 0xffff0000u));
-                o.z *= sigmoid(__uint_as_float(w.y << 16));
-                o.w *= sigmoid(__uint_as_float(w.y & 0xffff0000u));
+                o.x *= sigmoid_fast(__uint_as_float(z.x << 16));
+                o.y *= sigmoid_fast(__uint_as_float(z.x & 0xffff0000u));
+                o.z *= sigmoid_fast(__uint_as_float(z.y << 16));
+                o.w *= sigmoid_fast(__uint_as_float(z.y & 0xffff0000u));
             }
             *reinterpret_cast<uint2*>(p.out + at * D + col) = make_uint2(pack2<false>(o.x, o.y), pack2<false>(o.z, o.w));
-            if (p.lse && col == 0) p.lse[at] = (mx + log2f(sum)) * kLn2;
-        };
-        constexpr int ITEMS = BM * (CH / 4);          // float4 columns of a joined chunk
-        constexpr int PER = (ITEMS + 255) / 256;      // of one thread
-        float mx[PER], sum[PER];
-        uint2 gt[PER];
-#pragma unroll
-        for (int x = 0; x < PER; ++x) {
-            const int k = tid + x * 256, r = k / (CH / 4), col = (k % (CH / 4)) * 4;
-            mx[x] = sum[x] = 0.0f;
-            gt[x] = make_uint2(0, 0);
-            if (k < ITEMS && r < rows) {
-                const int w = r >> 4, rr = r & 15;
-                mx[x] = top_of(w, rr);
-#pragma unroll
-                for (int q = 0; q < NG; ++q) {
-                    const float mq = jm[(q * WM + w) * 16 + rr];
-                    if (mq != -INFINITY) sum[x] += jl[(q * WM + w) * 16 + rr] * exp2_fast(mq - mx[x]);
-                }
-                if (!split && p.gate.ptr) gt[x] = gate_of(r, col);
-                if (split && col == 0) {
-                    mine[BM * D + r] = mx[x];
-                    mine[BM * D + BM + r] = sum[x];
-                }
-            }
+            if (p.lse && col == 0) p.lse[at] = (w[kAttnMaxCtas + 1] + log2f(w[kAttnMaxCtas])) * kLn2;
         }
-#pragma unroll
-        for (int c = 0; c < D / CH; ++c) {
-            float* jb = jbuf + (c & 1) * (8 * 16 * JROW);
-            float* to = jb + warp * 16 * JROW;
-#pragma unroll
-            for (int x = 0; x < CH / 8; ++x) {
-                const int i = c * (CH / 8) + x;
-                if (!FP8) {
-                    *reinterpret_cast<float2*>(to + g * JROW + x * 8 + 2 * j) = make_float2(O[i][0], O[i][1]);
-                    *reinterpret_cast<float2*>(to + (g + 8) * JROW + x * 8 + 2 * j) = make_float2(O[i][2], O[i][3]);
-                } else if ((x & 1) == 0) {
-                    *reinterpret_cast<float4*>(to + g * JROW + x * 8 + 4 * j) = make_float4(O[i][0], O[i + 1][0], O[i][1], O[i + 1][1]);
-                    *reinterpret_cast<float4*>(to + (g + 8) * JROW + x * 8 + 4 * j) = make_float4(O[i][2], O[i + 1][2], O[i][3], O[i + 1][3]);
-                }
-            }
-            if (!meet()) return;
-#pragma unroll
-            for (int x = 0; x < PER; ++x) {
-                const int k = tid + x * 256, r = k / (CH / 4), col = (k % (CH / 4)) * 4;
-                if (k >= ITEMS || r >= rows) continue;
-                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                for (int q = 0; q < NG; ++q) {
-                    const float4 v = *reinterpret_cast<const float4*>(jb + ((q * WM + (r >> 4)) * 16 + (r & 15)) * JROW + col);
-                    o.x += v.x;
-                    o.y += v.y;
-                    o.z += v.z;
-                    o.w += v.w;
-                }
-                if (split) {
-                    *reinterpret_cast<float4*>(mine + r * D + c * CH + col) = o;
-                } else {
-                    const uint2 w = gt[x];
-                    if (p.gate.ptr && c + 1 < D / CH) gt[x] = gate_of(r, (c + 1) * CH + col);
-                    const float inv = p.sh.v_scale / sum[x];
-                    finish(r, c * CH + col, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv), mx[x], sum[x], w);
-                }
-            }
-        }
-        if (!split) continue;
-
-        // ---- a unit over several CTAs: the last of them to get here joins the pieces, in their order ----
-        __threadfence();
-        if (!meet()) return;
-        if (tid == 0) misc[14] = atomicAdd(p.counters + c0, 1u) == (unsigned)(c1 - c0);
-        if (!meet()) return;
-        if (!misc[14]) continue;
-        __threadfence();
-        const int pieces = c1 - c0 + 1;
-        auto part = [&](int i) {  // the i-th piece
-            const int c = c0 + i;
-            return p.partial + (size_t)(c * 2 + (i > 0 && (long)c * total / ctas > u.lo ? 0 : 1)) * PSTRIDE;
-        };
-        float* wt = jbuf;  // [16][kAttnMaxCtas] weights of the pieces, then their sum's inverse and the maximum
-        static_assert(16 * (kAttnMaxCtas + 2) * 4 <= Gm::JOINB, "weights");
-        for (int base = 0; base < rows; base += 16) {
-            const int n = min(16, rows - base);
-            if (!meet()) return;  // the weights' previous readers are done
-            for (int r = warp; r < n; r += kComputeWarps) {
-                float* w = wt + r * (kAttnMaxCtas + 2);
-                float top = -INFINITY, tot = 0.0f;
-                for (int i = lane; i < pieces; i += 32) {
-                    w[i] = __ldcg(part(i) + BM * D + base + r);
-                    top = fmaxf(top, w[i]);
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                for (int i = lane; i < pieces; i += 32) {
-                    w[i] = w[i] == -INFINITY ? 0.0f : exp2_fast(w[i] - top);
-                    tot = fmaf(w[i], __ldcg(part(i) + BM * D + BM + base + r), tot);
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-                if (lane == 0) {
-                    w[kAttnMaxCtas] = tot;
-                    w[kAttnMaxCtas + 1] = top;
-                }
-            }
-            if (!meet()) return;
-            for (int k = tid; k < n * (D / 4); k += 256) {
-                const int r = k / (D / 4), col = (k % (D / 4)) * 4;
-                const float* w = wt + r * (kAttnMaxCtas + 2);
-                const uint2 gw = p.gate.ptr ? gate_of(base + r, col) : make_uint2(0, 0);
-                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 16
-                for (int i = 0; i < pieces; ++i) {
-                    const float4 x = __ldcg(reinterpret_cast<const float4*>(part(i) + (base + r) * D + col));
-                    o.x = fmaf(w[i], x.x, o.x);
-                    o.y = fmaf(w[i], x.y, o.y);
-                    o.z = fmaf(w[i], x.z, o.z);
-                    o.w = fmaf(w[i], x.w, o.w);
-                }
-                const float inv = p.sh.v_scale / w[kAttnMaxCtas];
-                finish(base + r, col, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv), w[kAttnMaxCtas + 1], w[kAttnMaxCtas], gw);
-            }
-        }
-        if (tid == 0) p.counters[c0] = 0;
-        if (!meet()) return;
+        if (tid == 0) p.counters[u.c0] = 0;
+        if (!meet()) return;  // the next unit's weights go where these are
     }
+}
+
+// A tensor map over a pool of pages as [head][token / 8][128-byte block][token % 8][byte],
+// in boxes of `box` tokens of one head: the atoms that the kernels read, in their order.
+bool make_pool_map(CUtensorMap* m, void* pool, const AttnArgs& a, int row_bytes, int box) {
+    const int inner = row_bytes < 128 ? row_bytes : 128, blocks = row_bytes / inner, esz = a.sh.fp8 ? 1 : 2;
+    const cuuint64_t token = (cuuint64_t)a.sh.Hkv * row_bytes;
+    const cuuint64_t dims[5] = {(cuuint64_t)(inner / esz), 8, (cuuint64_t)blocks, (cuuint64_t)a.c.num_pages * a.sh.page_size / 8,
+                                (cuuint64_t)a.sh.Hkv};
+    const cuuint64_t strides[4] = {token, (cuuint64_t)inner, token * 8, (cuuint64_t)row_bytes};
+    const cuuint32_t boxes[5] = {(cuuint32_t)(inner / esz), 8, (cuuint32_t)blocks, (cuuint32_t)box / 8, 1};
+    return encode_tensor_map(m, a.sh.fp8, 5, pool, dims, strides, boxes, inner);
 }
 
 template <int D, bool FP8, int WM>
@@ -840,11 +947,20 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
     cudaError_t e = device_sms(&dev, &sms);
     if (e != cudaSuccess) return e;
     const size_t smem = Gm::SLOTS * (size_t)Gm::SLOTB + Gm::NQ * (size_t)Gm::QB + Gm::JOINB + Gm::FIXED + ((size_t)a.B + 1) * 4;
+    static_assert(4 * 32 * 4 + Gm::NQ * Gm::BM * 4 + (Gm::NQ + 3) * (int)sizeof(Piece) + (Gm::SLOTS + Gm::NQ + 1) * 8 +
+                      (Gm::SLOTS + Gm::NQ + 16) * 4 <= Gm::FIXED, "small data");
     static std::once_flag once[kMaxDevices];
+    static cudaError_t set[kMaxDevices];
     std::call_once(once[dev], [&] {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        set[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     });
-    if (e != cudaSuccess) return e;
+    if (set[dev] != cudaSuccess) return set[dev];
+    // TMA tiles of whole atoms when pages are whole atoms; otherwise row copies
+    int box = a.sh.page_size % 8 == 0 ? a.sh.page_size & -a.sh.page_size : 0;
+    if (box > Gm::ST) box = Gm::ST;
+    CUtensorMap map_k{}, map_v{};
+    if (box && !(make_pool_map(&map_k, a.c.k, a, Gm::ROWB, box) && make_pool_map(&map_v, a.c.v, a, Gm::ROWB, box)))
+        return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(sms < kAttnMaxCtas ? sms : kAttnMaxCtas));
     cfg.blockDim = dim3(kAttnThreads);
@@ -855,7 +971,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, a);
+    return cudaLaunchKernelEx(&cfg, kern, a, map_k, map_v, box);
 }
 
 // Row groups for `rows` query rows per key/value head.
