@@ -59,12 +59,13 @@ struct AttnArgs {
     uint16_t* out;
     float* lse;
     int32_t* err_flag;
-    unsigned int* counters;  // workspace: kAttnMaxCtas zeroed counters, left zeroed
+    unsigned int* counters;  // workspace: kAttnCounters zeroed counters, left zeroed
     float* partial;          // workspace: two partial results per CTA
 };
 
 // CTAs of the attention kernel (one per SM, at most this many) and the workspace.
 constexpr int kAttnMaxCtas = 192;
+constexpr int kAttnCounters = 3 * kAttnMaxCtas;  // arrivals at units, and at groups of their pieces
 constexpr int kAttnMaxBatch = 2048;
 int attn_row_tile(int d, bool fp8, int rows);  // query rows of a work unit for `rows` rows per key/value head
 int attn_token_tile(int d, bool fp8, int rows);

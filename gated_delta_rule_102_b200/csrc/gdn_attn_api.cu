@@ -188,7 +188,7 @@ gdn_status gdn_attn_decode(const gdn_attn_config* cfg, const gdn_kv_cache* cache
     a.lse = lse;
     a.err_flag = err_flag;
     a.counters = static_cast<unsigned int*>(workspace);
-    a.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + gdn::kAttnMaxCtas * sizeof(unsigned int));
+    a.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + gdn::kAttnCounters * sizeof(unsigned int));
     return from_cuda(gdn::launch_attn_decode(a, (cudaStream_t)stream));
 }
 

@@ -14,10 +14,10 @@
 // depend on which one that is. A CTA has at most two partial pieces, one at each end of
 // its share, so the workspace does not grow with the lengths.
 //
-// Within a CTA four warps load and eight compute. The ring holds slots of 16 KB, the keys
-// and values of ST tokens; each loading warp fills every fourth slot by itself and looks up
-// the pages of its next slot meanwhile, and the one that meets a unit's first slot also
-// brings the unit's queries and its description. When the page size is a multiple of 8 a
+// Within a CTA three warps load keys and values, one brings each unit's queries and its
+// description, and eight compute. The ring holds slots of 16 KB, the keys and values of ST
+// tokens; each loading warp fills every third slot by itself and looks up the pages of its
+// next slot meanwhile. When the page size is a multiple of 8 a
 // slot is a few TMA tiles (one for the keys and one for the values when a page holds whole
 // slots); any other page size takes 16-byte asynchronous copies, row by row. Both write
 // the same layout: atoms of 8 tokens by 128 bytes, 128-byte swizzle.
@@ -46,9 +46,20 @@ namespace gdn {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kLoadWarps = 4, kComputeWarps = 8, kAttnThreads = (kLoadWarps + kComputeWarps) * 32;
-constexpr int kUnitCost = 4;  // what a unit costs beside its slots, in slots (its queries, the join, the output)
-constexpr int kSingle = 4;    // a piece of so many slots or fewer is one token group's alone
+constexpr int kLoadWarps = 3, kComputeWarps = 8, kAttnThreads = (kLoadWarps + 1 + kComputeWarps) * 32;
+constexpr int kLaunchRegs = 168;
+#ifndef GDN_ATTN_UNIT_COST
+#define GDN_ATTN_UNIT_COST 4
+#endif
+#ifndef GDN_ATTN_SINGLE
+#define GDN_ATTN_SINGLE 4
+#endif
+#ifndef GDN_ATTN_MIN_SHARE
+#define GDN_ATTN_MIN_SHARE 8
+#endif
+constexpr int kUnitCost = GDN_ATTN_UNIT_COST;  // what a unit costs beside its slots, in slots (its queries, the join, the output)
+constexpr int kJoinFlat = 12, kJoinGroup = 8;  // pieces of a unit that one CTA joins at once, and groups of more
+constexpr int kSingle = GDN_ATTN_SINGLE;    // a piece of so many slots or fewer is one token group's alone
 
 // Geometry: D head size, WM row groups of 16 query rows.
 template <int D, bool FP8, int WM>
@@ -129,6 +140,11 @@ __device__ __forceinline__ uint32_t e4m3_to_half2(uint32_t w, bool high) {
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 template <bool HALF>
@@ -240,7 +256,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
     // a barrier's phase parity cannot tell a turn from the one two before it.
     int* freed = reinterpret_cast<int*>(cbar + 1);                // [SLOTS] warps that are done with a slot, all turns
     int* qfreed = freed + SLOTS;                                  // [NQ] the same for a unit's queries
-    int* misc = qfreed + NQ;                                      // [16] sums of the schedule's warps; 12, 13: last to arrive; 15: stop
+    int* misc = qfreed + NQ;                                      // [16] sums of the schedule's warps; 12: last to arrive; 15: stop
     int* prefix = misc + 16;                                      // [B + 1] cost of the sequences before each
     volatile int* stop = misc + 15;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -295,7 +311,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
     // As many CTAs as there are SMs, but no fewer slots a CTA than token groups. CTA c has the
     // places c * per + min(c, more) on: per of them, one more for the first ones. A unit takes
     // kUnitCost places, which no slot stands for, and one for each slot.
-    const int ctas = min((int)gridDim.x, (total + NG + kUnitCost - 1) / (NG + kUnitCost));
+    const int ctas = min((int)gridDim.x, (total + GDN_ATTN_MIN_SHARE - 1) / GDN_ATTN_MIN_SHARE);
     if ((int)blockIdx.x >= ctas) return;
     const int per = total / ctas, more = total - per * ctas;
     const int share_lo = blockIdx.x * per + min((int)blockIdx.x, more), share_hi = share_lo + per + ((int)blockIdx.x < more);
@@ -337,17 +353,90 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
         return true;
     };
 
+    // The block's registers (launched with kLaunchRegs a thread, which the launch checks) go to
+    // the warps that need them: 4 warps * 88 + 8 * 208 = 12 * 168.
+    if (warp >= kComputeWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
+
+    if (warp == kComputeWarps + kLoadWarps) {
+        // ================= queries =================
+        for (int ord = 0;; ++ord) {
+            const int rt = unit / Hkv, h = unit - rt * Hkv;
+            // the unit's queries: row r is token r / G, query head h * G + r % G; rows past the last
+            // are left as they are (a row's products touch no other row)
+            const int qs = ord % NQ, rows = min(BM, s.n * G - rt * BM);
+            const int inv_g = 65536 / G + 1;  // r / G = r * inv_g >> 16 for r < 320, G <= 16
+            if (!wait_count(qfreed + qs, ord / NQ * kComputeWarps)) return;
+            unsigned char* q = qbuf + qs * QB;
+            if (lane == 0) {
+                const int count = min(s.tiles - tile, share_hi - place - tile);
+                const int next = tile + count == s.tiles ? place + s.tiles + kUnitCost : share_hi;
+                pieces[qs] = Piece{s.n, s.first, s.past, s.lo, s.base, h, rt, tile, count, next >= share_hi,
+                                   cta_of(place), cta_of(place + s.tiles - 1)};
+                if (!FP8) mbar_arrive_expect_tx(qfull + qs, rows * D * 2);
+            }
+            __syncwarp();
+            auto row_of = [&](int r) {
+                const int rr = rt * BM + r, t = (rr * inv_g) >> 16;
+                return p.q.ptr + (size_t)(s.first + t) * p.q.row + (size_t)(h * G + rr - t * G) * p.q.head;
+            };
+            if (!FP8) {
+                for (int r = lane; r < rows; r += 32) tma_load_1d(q + r * QP, row_of(r), D * 2, qfull + qs);
+            } else {
+                // e4m3 keys become fp16, so the queries do too: a power of two per row brings its
+                // largest element to 2^14 .. 2^15, exact for every element above 2^-38 of that
+                constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes a row, rows at a time
+#pragma unroll 4
+                for (int r0 = 0; r0 < rows; r0 += RPW) {
+                    const int r = r0 + lane / LPR, c = lane % LPR;
+                    const uint4 w = r < rows ? __ldg(reinterpret_cast<const uint4*>(row_of(r)) + c) : make_uint4(0, 0, 0, 0);
+                    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) top = max(top, max(v[k] & 0x7fffu, (v[k] >> 16) & 0x7fffu));
+#pragma unroll
+                    for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const int e = top == 0 || top >= 0x7f80u ? 0 : max((int)(top >> 7), 1) - 127 - 14;
+                    // 2^-e: e is at most 113, and at least -140, where the exponent field ends
+                    const float up = __uint_as_float((uint32_t)(127 - max(e, -127)) << 23);
+                    uint32_t z[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) z[k] = pack2<true>(__uint_as_float(v[k] << 16) * up, __uint_as_float(v[k] & 0xffff0000u) * up);
+                    *reinterpret_cast<uint4*>(q + r * QP + c * 16) = make_uint4(z[0], z[1], z[2], z[3]);
+                    if (c == 0) qexp[qs * BM + r] = 1.0f / up;
+                }
+                mbar_arrive(qfull + qs);
+            }
+            if (p.gate.ptr) {  // the gates' lines into L2: they are read when the unit ends
+                for (int i = lane; i < rows * (D / 64); i += 32) {
+                    const int r = i / (D / 64), rr = rt * BM + r, t = (rr * inv_g) >> 16;
+                    const uint16_t* at = p.gate.ptr + (size_t)(s.first + t) * p.gate.row + (size_t)(h * G + rr - t * G) * p.gate.head;
+                    asm volatile("prefetch.global.L2 [%0];\n" ::"l"(at + i % (D / 64) * 64));
+                }
+            }
+            // the next unit with slots in the share
+            place += s.tiles + kUnitCost;
+            tile = 0;
+            if (place >= share_hi) return;
+            if (++unit == s.row_tiles * Hkv) {
+                unit = 0;
+                do {
+                    ++b;
+                } while (prefix[b + 1] == prefix[b]);
+                s = load_seq<BM, ST>(p, b, false);
+            }
+        }
+    }
+
     if (warp >= kComputeWarps) {
         // ================= loading =================
         const int pw = warp - kComputeWarps;
-        int ord = 0;
-        // `by` slots on; counts the units passed; false past the end of the share
+        // `by` slots on; false past the end of the share
         auto advance = [&](int by) {
             tile += by;
             while (place + tile < share_hi && tile >= s.tiles) {
                 tile -= s.tiles;
                 place += s.tiles + kUnitCost;
-                ++ord;
                 if (++unit == s.row_tiles * Hkv && place + tile < share_hi) {
                     unit = 0;
                     do {
@@ -421,53 +510,6 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                 }
                 cp_async_arrive(full + st);
             }
-            if (i == 0 || tile == 0) {
-                // the unit's queries: row r is token r / G, query head h * G + r % G; rows past the last
-                // are left as they are (a row's products touch no other row)
-                const int qs = ord % NQ, rows = min(BM, s.n * G - rt * BM);
-                const int inv_g = 65536 / G + 1;  // r / G = r * inv_g >> 16 for r < 320, G <= 16
-                if (!wait_count(qfreed + qs, ord / NQ * kComputeWarps)) break;
-                unsigned char* q = qbuf + qs * QB;
-                if (lane == 0) {
-                    const int count = min(s.tiles - tile, share_hi - place - tile);
-                    const int next = tile + count == s.tiles ? place + s.tiles + kUnitCost : share_hi;
-                    pieces[qs] = Piece{s.n, s.first, s.past, s.lo, s.base, h, rt, tile, count, next >= share_hi,
-                                       cta_of(place), cta_of(place + s.tiles - 1)};
-                    if (!FP8) mbar_arrive_expect_tx(qfull + qs, rows * D * 2);
-                }
-                __syncwarp();
-                auto row_of = [&](int r) {
-                    const int rr = rt * BM + r, t = (rr * inv_g) >> 16;
-                    return p.q.ptr + (size_t)(s.first + t) * p.q.row + (size_t)(h * G + rr - t * G) * p.q.head;
-                };
-                if (!FP8) {
-                    for (int r = lane; r < rows; r += 32) tma_load_1d(q + r * QP, row_of(r), D * 2, qfull + qs);
-                } else {
-                    // e4m3 keys become fp16, so the queries do too: a power of two per row brings its
-                    // largest element to 2^14 .. 2^15, exact for every element above 2^-38 of that
-                    constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes a row, rows at a time
-#pragma unroll 4
-                    for (int r0 = 0; r0 < BM; r0 += RPW) {
-                        const int r = r0 + lane / LPR, c = lane % LPR;
-                        const uint4 w = r < rows ? __ldg(reinterpret_cast<const uint4*>(row_of(r)) + c) : make_uint4(0, 0, 0, 0);
-                        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-                        uint32_t top = 0;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) top = max(top, max(v[k] & 0x7fffu, (v[k] >> 16) & 0x7fffu));
-#pragma unroll
-                        for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        const int e = top == 0 || top >= 0x7f80u ? 0 : max((int)(top >> 7), 1) - 127 - 14;
-                        // 2^-e: e is at most 113, and at least -140, where the exponent field ends
-                        const float up = __uint_as_float((uint32_t)(127 - max(e, -127)) << 23);
-                        uint32_t z[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) z[k] = pack2<true>(__uint_as_float(v[k] << 16) * up, __uint_as_float(v[k] & 0xffff0000u) * up);
-                        *reinterpret_cast<uint4*>(q + r * QP + c * 16) = make_uint4(z[0], z[1], z[2], z[3]);
-                        if (c == 0) qexp[qs * BM + r] = 1.0f / up;
-                    }
-                    mbar_arrive(qfull + qs);
-                }
-            }
             more_slots = advance(kLoadWarps);
             if (more_slots) find_tokens();
         }
@@ -510,10 +552,11 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
         const int lo0 = p.sh.window > 0 ? u.past + t0 + 1 - p.sh.window : 0;
         const int lo1 = p.sh.window > 0 ? u.past + t1 + 1 - p.sh.window : 0;
         const int all_lo = p.sh.window > 0 ? max(0, kv_len - p.sh.window) : 0, all_hi = u.past + 1;
-        float e0 = 1.0f, e1 = 1.0f;
+        // what a product is multiplied by: to log2 units, or to twice the cap's argument
+        float f0 = capped ? cap_in : to_log2, f1 = f0;
         if (FP8) {
-            e0 = qexp[qs * BM + wm * 16 + g];
-            e1 = qexp[qs * BM + wm * 16 + g + 8];
+            f0 *= qexp[qs * BM + wm * 16 + g];
+            f1 *= qexp[qs * BM + wm * 16 + g + 8];
         }
         float O[ND][4];
 #pragma unroll
@@ -543,20 +586,31 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                 fence_proxy_async_smem();  // before the slot is filled again
                 __syncwarp();
             }
-            float S[KS * 2][4];
+            // with few tokens a slot, even and odd steps go to accumulators of their own (a product waits
+            // for the one before it of the same accumulator)
+            constexpr int SETS = KS <= 2 && !FP8 ? 2 : 1;
+            float S[SETS * KS * 2][4];
 #pragma unroll
-            for (int x = 0; x < KS * 2; ++x) S[x][0] = S[x][1] = S[x][2] = S[x][3] = 0.0f;
+            for (int x = 0; x < SETS * KS * 2; ++x) S[x][0] = S[x][1] = S[x][2] = S[x][3] = 0.0f;
             if (!FP8) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
+                    const int o = SETS == 2 ? (kk & 1) * KS * 2 : 0;
                     uint32_t a[4];
                     ldsm4(a, qaddr + (wm * 16 + (lane & 15)) * QP + (kk * 2 + (lane >> 4)) * 16);
 #pragma unroll
                     for (int x = 0; x < KS; ++x) {
                         uint32_t v[4];
                         ldsm4(v, ks + chunk_at<CPR>(x * 16 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)));
-                        mma<false>(S[2 * x], a, v[0], v[1]);
-                        mma<false>(S[2 * x + 1], a, v[2], v[3]);
+                        mma<false>(S[o + 2 * x], a, v[0], v[1]);
+                        mma<false>(S[o + 2 * x + 1], a, v[2], v[3]);
+                    }
+                }
+                if (SETS == 2) {
+#pragma unroll
+                    for (int x = 0; x < KS * 2; ++x) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) S[x][e] += S[(SETS - 1) * KS * 2 + x][e];
                     }
                 }
             } else {
@@ -587,21 +641,35 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                 }
             }
             float mx0 = m[0], mx1 = m[1];
+            if (capped) {
 #pragma unroll
-            for (int x = 0; x < KS * 2; ++x) {
+                for (int x = 0; x < KS * 2; ++x) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float y = FP8 ? S[x][e] * (e < 2 ? e0 : e1) : S[x][e];
-                    if (capped) y = 1.0f - __fdividef(2.0f, 1.0f + exp2_fast(y * cap_in));  // tanh
-                    y *= to_log2;
-                    if (!whole) {
+                    for (int e = 0; e < 4; ++e)  // c tanh(y) = c - 2 c / (1 + e^2y)
+                        S[x][e] = fmaf(-2.0f * to_log2, rcp_fast(1.0f + exp2_fast(S[x][e] * (e < 2 ? f0 : f1))), to_log2);
+                }
+            } else {
+#pragma unroll
+                for (int x = 0; x < KS * 2; ++x) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) S[x][e] *= e < 2 ? f0 : f1;
+                }
+            }
+            if (!whole) {
+#pragma unroll
+                for (int x = 0; x < KS * 2; ++x) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
                         const int pos = pos0 + x * 8 + 2 * j + (e & 1);
                         const bool in = e < 2 ? pos < hi0 && pos >= lo0 : pos < hi1 && pos >= lo1;
-                        y = in ? y : -INFINITY;
+                        S[x][e] = in ? S[x][e] : -INFINITY;
                     }
-                    S[x][e] = y;
-                    if (e < 2) mx0 = fmaxf(mx0, y); else mx1 = fmaxf(mx1, y);
                 }
+            }
+#pragma unroll
+            for (int x = 0; x < KS * 2; ++x) {
+                mx0 = fmaxf(mx0, fmaxf(S[x][0], S[x][1]));
+                mx1 = fmaxf(mx1, fmaxf(S[x][2], S[x][3]));
             }
             mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
             mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
@@ -609,15 +677,15 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
             mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
             const float ref0 = mx0 == -INFINITY ? 0.0f : mx0, ref1 = mx1 == -INFINITY ? 0.0f : mx1;  // nothing seen yet
             if (__any_sync(0xffffffffu, mx0 != m[0] || mx1 != m[1])) {
-                const float f0 = exp2_fast(m[0] - ref0), f1 = exp2_fast(m[1] - ref1);
-                l[0] *= f0;
-                l[1] *= f1;
+                const float a0 = exp2_fast(m[0] - ref0), a1 = exp2_fast(m[1] - ref1);
+                l[0] *= a0;
+                l[1] *= a1;
 #pragma unroll
                 for (int x = 0; x < ND; ++x) {
-                    O[x][0] *= f0;
-                    O[x][1] *= f0;
-                    O[x][2] *= f1;
-                    O[x][3] *= f1;
+                    O[x][0] *= a0;
+                    O[x][1] *= a0;
+                    O[x][2] *= a1;
+                    O[x][3] *= a1;
                 }
                 m[0] = mx0;
                 m[1] = mx1;
@@ -681,16 +749,15 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
             } else {
 #pragma unroll 1
                 for (int t = 0; t < ST; ++t) {
-                    float p0 = 0.0f, p1 = 0.0f;
+                    uint32_t b0 = 0, b1 = 0;  // by masks: an index known at run time only would put S into local memory
 #pragma unroll
                     for (int x = 0; x < KS * 2; ++x) {
-                        if (x == (t >> 3)) {
-                            p0 = (t & 1) ? S[x][1] : S[x][0];
-                            p1 = (t & 1) ? S[x][3] : S[x][2];
-                        }
+                        const uint32_t even = x == (t >> 3) && !(t & 1) ? ~0u : 0u, odd = x == (t >> 3) && (t & 1) ? ~0u : 0u;
+                        b0 |= (__float_as_uint(S[x][0]) & even) | (__float_as_uint(S[x][1]) & odd);
+                        b1 |= (__float_as_uint(S[x][2]) & even) | (__float_as_uint(S[x][3]) & odd);
                     }
-                    p0 = __shfl_sync(0xffffffffu, p0, (lane & ~3) | ((t >> 1) & 3));
-                    p1 = __shfl_sync(0xffffffffu, p1, (lane & ~3) | ((t >> 1) & 3));
+                    const float p0 = __uint_as_float(__shfl_sync(0xffffffffu, b0, (lane & ~3) | ((t >> 1) & 3)));
+                    const float p1 = __uint_as_float(__shfl_sync(0xffffffffu, b1, (lane & ~3) | ((t >> 1) & 3)));
                     const int pos = pos0 + t;
                     const bool in0 = pos < hi0 && pos >= lo0, in1 = pos < hi1 && pos >= lo1;
 #pragma unroll
@@ -853,77 +920,107 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
     }
 
     // ---- units over several CTAs: the last of them to get here joins the pieces, in their order ----
+    // More than kJoinFlat pieces are joined in groups of kJoinGroup first (by the last CTA of the
+    // group, into its first piece's place), then the groups: at 74 pieces of 8 KB one CTA alone
+    // would read 600 KB.
     if (!split_first && !split_last) return;
     __threadfence();
     if (!meet()) return;
-    if (tid < 2 && (tid == 0 ? split_first : split_last)) {
-        const Piece& u = pieces[NQ + tid];
-        misc[12 + tid] = atomicAdd(p.counters + u.c0, 1u) == (unsigned)(u.c1 - u.c0);
-    }
-    if (!meet()) return;
+    float* wt = reinterpret_cast<float*>(ring);  // [BM][WP] weights of the pieces, their sum and maximum
+    constexpr int WP = kAttnMaxCtas + 2;
+    static_assert(BM * WP * 4 <= SLOTS * Gm::SLOTB, "weights");
     for (int which = 0; which < 2; ++which) {
-        if (!(which ? split_last : split_first) || !misc[12 + which]) continue;
-        __threadfence();
+        if (!(which ? split_last : split_first)) continue;
         const Piece u = pieces[NQ + which];
-        const int rows = min(BM, u.n * G - u.rt * BM), count = u.c1 - u.c0 + 1;
-        auto part = [&](int i) -> const float* { return p.partial + (size_t)((u.c0 + i) * 2 + (i == 0)) * PSTRIDE; };
-        float* wt = reinterpret_cast<float*>(ring);  // [BM][kAttnMaxCtas + 2] weights of the pieces, their sum and maximum
-        constexpr int WP = kAttnMaxCtas + 2;
-        static_assert(BM * WP * 4 <= SLOTS * Gm::SLOTB, "weights");
-        if (!meet()) return;
-        for (int r = warp; r < rows; r += kComputeWarps) {
-            float* w = wt + r * WP;
-            float top = -INFINITY, tot = 0.0f;
-            for (int i = lane; i < count; i += 32) {
-                w[i] = __ldcg(part(i) + BM * D + r);
-                top = fmaxf(top, w[i]);
-            }
+        const int rows = min(BM, u.n * G - u.rt * BM), all = u.c1 - u.c0 + 1;
+        auto place_of = [&](int i) { return p.partial + (size_t)((u.c0 + i) * 2 + (i == 0)) * PSTRIDE; };
+        const bool flat = all <= kJoinFlat;
+        for (int level = flat ? 1 : 0; level < 2; ++level) {
+            // level 0: this CTA's group of pieces; level 1: all pieces, or the groups' first places
+            const int step = level == 1 && !flat ? kJoinGroup : 1;
+            const int from = level == 0 ? ((int)blockIdx.x - u.c0) / kJoinGroup * kJoinGroup : 0;
+            const int count = level == 0 ? min(kJoinGroup, all - from) : (all + step - 1) / step;
+            unsigned int* counter = p.counters + (level == 1 ? u.c0 : kAttnMaxCtas + (u.c0 + from) * 2 + (from == 0));
+            if (tid == 0) misc[12] = atomicAdd(counter, 1u) == (unsigned)(count - 1);
+            if (!meet()) return;
+            if (!misc[12]) break;  // (written next after another meeting)
+            __threadfence();
+            auto part = [&](int i) -> const float* { return place_of(from + i * step); };
+            for (int r = warp; r < rows; r += kComputeWarps) {
+                float* w = wt + r * WP;
+                float top = -INFINITY, tot = 0.0f;
+                for (int i = lane; i < count; i += 32) {
+                    w[i] = __ldcg(part(i) + BM * D + r);
+                    top = fmaxf(top, w[i]);
+                }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            for (int i = lane; i < count; i += 32) {
-                w[i] = w[i] == -INFINITY ? 0.0f : exp2_fast(w[i] - top);
-                tot = fmaf(w[i], __ldcg(part(i) + BM * D + BM + r), tot);
-            }
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                for (int i = lane; i < count; i += 32) {
+                    w[i] = w[i] == -INFINITY ? 0.0f : exp2_fast(w[i] - top);
+                    tot = fmaf(w[i], __ldcg(part(i) + BM * D + BM + r), tot);
+                }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-            if (lane == 0) {
-                w[kAttnMaxCtas] = tot;
-                w[kAttnMaxCtas + 1] = top;
+                for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+                if (lane == 0) {
+                    w[kAttnMaxCtas] = tot;
+                    w[kAttnMaxCtas + 1] = top;
+                }
             }
+            if (!meet()) return;
+            for (int k = tid; k < rows * (D / 4); k += kComputeWarps * 32) {
+                const int r = k / (D / 4), col = (k % (D / 4)) * 4;
+                const float* w = wt + r * WP;
+                const float* src = part(0) + r * D + col;
+                const float* rest = count > 1 ? part(1) + r * D + col : src;
+                const size_t stride = (size_t)step * 2 * PSTRIDE;
+                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int i0 = 0; i0 < count; i0 += 10) {
+                    float4 x[10];
+#pragma unroll
+                    for (int i = 0; i < 10; ++i) {
+                        const float* at = i0 + i == 0 ? src : rest + (size_t)(i0 + i - 1) * stride;
+                        x[i] = i0 + i < count ? __ldcg(reinterpret_cast<const float4*>(at)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 10; ++i) {
+                        const float f = i0 + i < count ? w[i0 + i] : 0.0f;
+                        o.x = fmaf(f, x[i].x, o.x);
+                        o.y = fmaf(f, x[i].y, o.y);
+                        o.z = fmaf(f, x[i].z, o.z);
+                        o.w = fmaf(f, x[i].w, o.w);
+                    }
+                }
+                if (level == 0) {
+                    *reinterpret_cast<float4*>(place_of(from) + r * D + col) = o;
+                    continue;
+                }
+                const int rr = u.rt * BM + r, t = rr / G, head = u.h * G + rr - t * G;
+                const size_t row = (size_t)u.first + t, at = row * p.sh.Hq + head;
+                const float inv = p.sh.v_scale / w[kAttnMaxCtas];
+                o.x *= inv;
+                o.y *= inv;
+                o.z *= inv;
+                o.w *= inv;
+                if (p.gate.ptr) {
+                    const uint2 z = __ldg(reinterpret_cast<const uint2*>(p.gate.ptr + row * p.gate.row + (size_t)head * p.gate.head + col));
+                    o.x *= sigmoid_fast(__uint_as_float(z.x << 16));
+                    o.y *= sigmoid_fast(__uint_as_float(z.x & 0xffff0000u));
+                    o.z *= sigmoid_fast(__uint_as_float(z.y << 16));
+                    o.w *= sigmoid_fast(__uint_as_float(z.y & 0xffff0000u));
+                }
+                *reinterpret_cast<uint2*>(p.out + at * D + col) = make_uint2(pack2<false>(o.x, o.y), pack2<false>(o.z, o.w));
+                if (p.lse && col == 0) p.lse[at] = (w[kAttnMaxCtas + 1] + log2f(w[kAttnMaxCtas])) * kLn2;
+            }
+            if (tid == 0) *counter = 0;
+            if (level == 0 && tid < rows) {  // the group's maximum and sum, in place of its first piece's
+                float* to = place_of(from) + BM * D;
+                to[tid] = wt[tid * WP + kAttnMaxCtas + 1];
+                to[BM + tid] = wt[tid * WP + kAttnMaxCtas];
+            }
+            if (level == 0) __threadfence();
+            if (!meet()) return;  // the next weights go where these are
         }
-        if (!meet()) return;
-        for (int k = tid; k < rows * (D / 4); k += kComputeWarps * 32) {
-            const int r = k / (D / 4), col = (k % (D / 4)) * 4;
-            const float* w = wt + r * WP;
-            const int rr = u.rt * BM + r, t = rr / G, head = u.h * G + rr - t * G;
-            const size_t row = (size_t)u.first + t, at = row * p.sh.Hq + head;
-            uint2 z = make_uint2(0, 0);
-            if (p.gate.ptr) z = __ldg(reinterpret_cast<const uint2*>(p.gate.ptr + row * p.gate.row + (size_t)head * p.gate.head + col));
-            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-            for (int i = 0; i < count; ++i) {
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(part(i) + r * D + col));
-                o.x = fmaf(w[i], x.x, o.x);
-                o.y = fmaf(w[i], x.y, o.y);
-                o.z = fmaf(w[i], x.z, o.z);
-                o.w = fmaf(w[i], x.w, o.w);
-            }
-            const float inv = p.sh.v_scale / w[kAttnMaxCtas];
-            o.x *= inv;
-            o.y *= inv;
-            o.z *= inv;
-            o.w *= inv;
-            if (p.gate.ptr) {
-                o.x *= sigmoid_fast(__uint_as_float(z.x << 16));
-                o.y *= sigmoid_fast(__uint_as_float(z.x & 0xffff0000u));
-                o.z *= sigmoid_fast(__uint_as_float(z.y << 16));
-                o.w *= sigmoid_fast(__uint_as_float(z.y & 0xffff0000u));
-            }
-            *reinterpret_cast<uint2*>(p.out + at * D + col) = make_uint2(pack2<false>(o.x, o.y), pack2<false>(o.z, o.w));
-            if (p.lse && col == 0) p.lse[at] = (w[kAttnMaxCtas + 1] + log2f(w[kAttnMaxCtas])) * kLn2;
-        }
-        if (tid == 0) p.counters[u.c0] = 0;
-        if (!meet()) return;  // the next unit's weights go where these are
+        if (which == 0 && split_last && !meet()) return;  // misc[12] is written again
     }
 }
 
@@ -952,7 +1049,12 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
     static std::once_flag once[kMaxDevices];
     static cudaError_t set[kMaxDevices];
     std::call_once(once[dev], [&] {
-        set[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        cudaFuncAttributes attr;
+        set[dev] = cudaFuncGetAttributes(&attr, kern);
+        // the kernel hands registers from one role to the others: fewer at the launch and it would wait for good
+        if (set[dev] == cudaSuccess && attr.numRegs != kLaunchRegs) set[dev] = cudaErrorLaunchOutOfResources;
+        if (set[dev] == cudaSuccess)
+            set[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     });
     if (set[dev] != cudaSuccess) return set[dev];
     // TMA tiles of whole atoms when pages are whole atoms; otherwise row copies
@@ -1010,7 +1112,7 @@ int attn_token_tile(int d, bool fp8, int rows) {
     return with_geometry(d, fp8, rows, [](auto g) { return decltype(g)::ST; });
 }
 size_t attn_workspace_bytes(int d, bool fp8, int rows) {
-    return kAttnMaxCtas * sizeof(unsigned int) + (size_t)kAttnMaxCtas * 2 * attn_row_tile(d, fp8, rows) * (d + 2) * sizeof(float);
+    return kAttnCounters * sizeof(unsigned int) + (size_t)kAttnMaxCtas * 2 * attn_row_tile(d, fp8, rows) * (d + 2) * sizeof(float);
 }
 
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t stream) {

@@ -201,7 +201,7 @@ def check_attn(L, window=0, softcap=0.0, gated=False, k=None, v=None, q=None, la
     first = out.clone(), lse.clone()
     gdn.gdn_attn_decode(*args, **kw)
     assert torch.equal(view(first[0], BF16), view(out, BF16)) and torch.equal(first[1].view(I32), lse.view(I32))
-    assert int(L.err) == 0 and not ws[:192].any()
+    assert int(L.err) == 0 and not ws[:576].any()
     scale = 1.0 / math.sqrt(d)
     worst = 0.0
     flat = lambda x: x.reshape(L.total, Hq, -1)  # noqa: E731
@@ -328,7 +328,7 @@ def test_attn_skips_and_flags_bad_sequences():
         for b in range(B):
             if b not in unspecified:
                 assert bool((out[b] == -7.0).all()) == (b in rows), b
-        assert not ws[:192].any()
+        assert not ws[:576].any()
     go(0, [])
     slots = L.slots.clone(); slots[1] = -1; slots[2] = 1000
     go(gdn.GDN_DEVICE_ERR_SLOT_RANGE, [1, 2], slots=slots)
