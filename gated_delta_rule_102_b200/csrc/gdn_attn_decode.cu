@@ -49,7 +49,16 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kLoadWarps = 3, kComputeWarps = 8, kAttnThreads = (kLoadWarps + 1 + kComputeWarps) * 32;
 constexpr int kLaunchRegs = 168;
 #ifndef GDN_ATTN_UNIT_COST
-#define GDN_ATTN_UNIT_COST 4
+#define GDN_ATTN_UNIT_COST 14
+#endif
+#ifndef GDN_ATTN_KU
+#define GDN_ATTN_KU 2
+#endif
+#ifndef GDN_ATTN_NQ
+#define GDN_ATTN_NQ 6
+#endif
+#ifndef GDN_ATTN_SHORT_COST
+#define GDN_ATTN_SHORT_COST 4
 #endif
 #ifndef GDN_ATTN_SINGLE
 #define GDN_ATTN_SINGLE 4
@@ -57,7 +66,7 @@ constexpr int kLaunchRegs = 168;
 #ifndef GDN_ATTN_MIN_SHARE
 #define GDN_ATTN_MIN_SHARE 8
 #endif
-constexpr int kUnitCost = GDN_ATTN_UNIT_COST;  // what a unit costs beside its slots, in slots (its queries, the join, the output)
+constexpr int kShortCost = GDN_ATTN_SHORT_COST, kUnitCost = GDN_ATTN_UNIT_COST;  // what a unit costs beside its slots, in slots (its queries, the join, the output)
 constexpr int kJoinFlat = 12, kJoinGroup = 8;  // pieces of a unit that one CTA joins at once, and groups of more
 constexpr int kSingle = GDN_ATTN_SINGLE;    // a piece of so many slots or fewer is one token group's alone
 
@@ -67,7 +76,7 @@ struct Geo {
     static constexpr int ROWB = D * (FP8 ? 1 : 2);  // bytes of a token's key (value)
     static constexpr int SLOTB = 16 * 1024, HALF = SLOTB / 2;
     static constexpr int ST = HALF / ROWB;          // tokens of a slot
-    static constexpr int KS = ST / 16;
+    static constexpr int KU = ST >= 32 ? GDN_ATTN_KU : 1, SUB = KU * 16;  // tokens that a warp works on at a time
     static constexpr int CS = D == 256 ? 2 : 1;     // column halves
     static constexpr int ND = D / CS / 8;           // 8-column tiles of a warp's output
     static constexpr int NG = kComputeWarps / (WM * CS);  // token groups
@@ -75,13 +84,13 @@ struct Geo {
     static constexpr int BM = 16 * WM;
     static constexpr int QP = D * 2 + 16;           // bytes from one query row to the next: eight rows, eight bank groups
     static constexpr int QB = BM * QP;
-    static constexpr int NQ = WM == 4 ? 2 : 3;      // units whose queries are held
+    static constexpr int NQ = WM == 4 ? 2 : (WM == 2 ? 3 : GDN_ATTN_NQ);  // units whose queries are held
     static constexpr int CPR = ROWB / 16;           // 16-byte chunks of a token row
     static constexpr int JOINB = NG == 1 ? 0 : (kComputeWarps / 2) * 32 * ND * 16;
     static constexpr int FIXED = 4096;              // everything small (checked at the launch)
     static constexpr int FIT = (227 * 1024 - (kAttnMaxBatch + 1) * 4 - FIXED - JOINB - NQ * QB) / SLOTB;
     static constexpr int SLOTS = FIT > 12 ? 12 : FIT;
-    static_assert(SLOTS >= 8 && KS >= 1 && NG >= 1, "ring");
+    static_assert(SLOTS >= 8 && ST % SUB == 0 && NG >= 1, "ring");
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
@@ -170,6 +179,7 @@ __device__ __forceinline__ int chunk_at(int r, int c) {
 struct Seq {
     int n, first, past, slot;  // tokens of this call, their first row, tokens before them
     int lo, base, tiles;       // first position any row attends, the slots' first position, slots
+    int cost;                  // places of a unit in the schedule beside its slots'
     int row_tiles;
 };
 
@@ -177,6 +187,7 @@ template <int BM, int ST>
 __device__ __forceinline__ Seq load_seq(const AttnArgs& p, int b, bool report) {
     Seq s;
     s.tiles = 0;
+    s.cost = 0;
     s.row_tiles = 0;
     s.slot = __ldg(p.slots + b);
     s.first = b * p.T;
@@ -206,6 +217,7 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& p, int b, bool report) {
     if (p.sh.window > 0 && s.past + 1 > p.sh.window) s.lo = s.past + 1 - p.sh.window;
     s.base = s.lo & ~(ST - 1);
     s.tiles = (s.past + s.n - s.base + ST - 1) / ST;
+    s.cost = s.tiles <= kSingle ? kShortCost : kUnitCost;
     s.row_tiles = (s.n * p.sh.G + BM - 1) / BM;
     return s;
 }
@@ -240,7 +252,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v, const int box) {
     using Gm = Geo<D, FP8, WM>;
-    constexpr int BM = Gm::BM, ST = Gm::ST, KS = Gm::KS, NG = Gm::NG, CS = Gm::CS, CPR = Gm::CPR, SLOTS = Gm::SLOTS;
+    constexpr int BM = Gm::BM, ST = Gm::ST, KU = Gm::KU, SUB = Gm::SUB, NG = Gm::NG, CS = Gm::CS, CPR = Gm::CPR, SLOTS = Gm::SLOTS;
     constexpr int NQ = Gm::NQ, QB = Gm::QB, QP = Gm::QP, HALF = Gm::HALF, ND = Gm::ND;
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char* ring = smem;
@@ -286,7 +298,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
         int t = 0;
         if (b < p.B) {
             const Seq s = load_seq<BM, ST>(p, b, blockIdx.x == 0);
-            if (s.tiles > 0) t = (s.tiles + kUnitCost) * s.row_tiles * Hkv;
+            t = (s.tiles + s.cost) * s.row_tiles * Hkv;
         }
         int x = t;
 #pragma unroll
@@ -310,7 +322,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
     __syncthreads();
     // As many CTAs as there are SMs, but no fewer slots a CTA than token groups. CTA c has the
     // places c * per + min(c, more) on: per of them, one more for the first ones. A unit takes
-    // kUnitCost places, which no slot stands for, and one for each slot.
+    // some places that no slot stands for (what it costs beside its slots) and one for each slot.
     const int ctas = min((int)gridDim.x, (total + GDN_ATTN_MIN_SHARE - 1) / GDN_ATTN_MIN_SHARE);
     if ((int)blockIdx.x >= ctas) return;
     const int per = total / ctas, more = total - per * ctas;
@@ -328,11 +340,25 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
         }
     }
     Seq s = load_seq<BM, ST>(p, b, false);  // the last sequence that starts at or before the share: it has units
-    int unit = (share_lo - prefix[b]) / (s.tiles + kUnitCost);  // row_tile * Hkv + kv head
-    int place = prefix[b] + unit * (s.tiles + kUnitCost) + kUnitCost;  // of the unit's first slot
+    int unit = (share_lo - prefix[b]) / (s.tiles + s.cost);  // row_tile * Hkv + kv head
+    int place = prefix[b] + unit * (s.tiles + s.cost) + s.cost;  // of the unit's first slot
     int tile = max(share_lo - place, 0);
     if (place + tile >= share_hi) return;  // nothing but a unit's overhead
 
+    // to the next unit; false when its slots lie past the share
+    auto next_unit = [&] {
+        place += s.tiles;  // the unit's end
+        if (place >= share_hi) return false;
+        if (++unit == s.row_tiles * Hkv) {
+            unit = 0;
+            do {
+                ++b;
+            } while (prefix[b + 1] == prefix[b]);
+            s = load_seq<BM, ST>(p, b, false);
+        }
+        place += s.cost;
+        return place < share_hi;
+    };
     auto give_up = [&] { return *stop != 0; };
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (mbar_wait_deadline(bar, parity, kWaitTimeoutCycles, give_up)) return true;
@@ -360,25 +386,27 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
 
     if (warp == kComputeWarps + kLoadWarps) {
         // ================= queries =================
-        for (int ord = 0;; ++ord) {
-            const int rt = unit / Hkv, h = unit - rt * Hkv;
+        bool more_units = true;
+        for (int ord = 0; more_units; ++ord) {
+            const Seq c = s;
+            const int rt = unit / Hkv, h = unit - rt * Hkv, at = place, from = tile;
+            more_units = next_unit();  // before this one is described: it may be the last
+            tile = 0;
             // the unit's queries: row r is token r / G, query head h * G + r % G; rows past the last
             // are left as they are (a row's products touch no other row)
-            const int qs = ord % NQ, rows = min(BM, s.n * G - rt * BM);
+            const int qs = ord % NQ, rows = min(BM, c.n * G - rt * BM);
             const int inv_g = 65536 / G + 1;  // r / G = r * inv_g >> 16 for r < 320, G <= 16
             if (!wait_count(qfreed + qs, ord / NQ * kComputeWarps)) return;
             unsigned char* q = qbuf + qs * QB;
             if (lane == 0) {
-                const int count = min(s.tiles - tile, share_hi - place - tile);
-                const int next = tile + count == s.tiles ? place + s.tiles + kUnitCost : share_hi;
-                pieces[qs] = Piece{s.n, s.first, s.past, s.lo, s.base, h, rt, tile, count, next >= share_hi,
-                                   cta_of(place), cta_of(place + s.tiles - 1)};
+                pieces[qs] = Piece{c.n, c.first, c.past, c.lo, c.base, h, rt, from, min(c.tiles - from, share_hi - at - from),
+                                   !more_units, cta_of(at), cta_of(at + c.tiles - 1)};
                 if (!FP8) mbar_arrive_expect_tx(qfull + qs, rows * D * 2);
             }
             __syncwarp();
             auto row_of = [&](int r) {
                 const int rr = rt * BM + r, t = (rr * inv_g) >> 16;
-                return p.q.ptr + (size_t)(s.first + t) * p.q.row + (size_t)(h * G + rr - t * G) * p.q.head;
+                return p.q.ptr + (size_t)(c.first + t) * p.q.row + (size_t)(h * G + rr - t * G) * p.q.head;
             };
             if (!FP8) {
                 for (int r = lane; r < rows; r += 32) tma_load_1d(q + r * QP, row_of(r), D * 2, qfull + qs);
@@ -386,46 +414,44 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                 // e4m3 keys become fp16, so the queries do too: a power of two per row brings its
                 // largest element to 2^14 .. 2^15, exact for every element above 2^-38 of that
                 constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes a row, rows at a time
-#pragma unroll 4
-                for (int r0 = 0; r0 < rows; r0 += RPW) {
-                    const int r = r0 + lane / LPR, c = lane % LPR;
-                    const uint4 w = r < rows ? __ldg(reinterpret_cast<const uint4*>(row_of(r)) + c) : make_uint4(0, 0, 0, 0);
-                    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-                    uint32_t top = 0;
+                for (int r0 = 0; r0 < rows; r0 += 8 * RPW) {  // eight loads in flight
+                    uint4 in[8];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) top = max(top, max(v[k] & 0x7fffu, (v[k] >> 16) & 0x7fffu));
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = r0 + i * RPW + lane / LPR;
+                        in[i] = r < rows ? __ldg(reinterpret_cast<const uint4*>(row_of(r)) + lane % LPR) : make_uint4(0, 0, 0, 0);
+                    }
 #pragma unroll
-                    for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    const int e = top == 0 || top >= 0x7f80u ? 0 : max((int)(top >> 7), 1) - 127 - 14;
-                    // 2^-e: e is at most 113, and at least -140, where the exponent field ends
-                    const float up = __uint_as_float((uint32_t)(127 - max(e, -127)) << 23);
-                    uint32_t z[4];
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = r0 + i * RPW + lane / LPR, ch = lane % LPR;
+                        if (r0 + i * RPW >= rows) break;  // the same for every lane
+                        const uint32_t v[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
+                        uint32_t top = 0;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) z[k] = pack2<true>(__uint_as_float(v[k] << 16) * up, __uint_as_float(v[k] & 0xffff0000u) * up);
-                    *reinterpret_cast<uint4*>(q + r * QP + c * 16) = make_uint4(z[0], z[1], z[2], z[3]);
-                    if (c == 0) qexp[qs * BM + r] = 1.0f / up;
+                        for (int k = 0; k < 4; ++k) top = max(top, max(v[k] & 0x7fffu, (v[k] >> 16) & 0x7fffu));
+#pragma unroll
+                        for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        const int e = top == 0 || top >= 0x7f80u ? 0 : max((int)(top >> 7), 1) - 127 - 14;
+                        // 2^-e: e is at most 113, and at least -140, where the exponent field ends
+                        const float up = __uint_as_float((uint32_t)(127 - max(e, -127)) << 23);
+                        uint32_t z[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) z[k] = pack2<true>(__uint_as_float(v[k] << 16) * up, __uint_as_float(v[k] & 0xffff0000u) * up);
+                        *reinterpret_cast<uint4*>(q + r * QP + ch * 16) = make_uint4(z[0], z[1], z[2], z[3]);
+                        if (ch == 0) qexp[qs * BM + r] = 1.0f / up;
+                    }
                 }
                 mbar_arrive(qfull + qs);
             }
             if (p.gate.ptr) {  // the gates' lines into L2: they are read when the unit ends
                 for (int i = lane; i < rows * (D / 64); i += 32) {
                     const int r = i / (D / 64), rr = rt * BM + r, t = (rr * inv_g) >> 16;
-                    const uint16_t* at = p.gate.ptr + (size_t)(s.first + t) * p.gate.row + (size_t)(h * G + rr - t * G) * p.gate.head;
-                    asm volatile("prefetch.global.L2 [%0];\n" ::"l"(at + i % (D / 64) * 64));
+                    const uint16_t* line = p.gate.ptr + (size_t)(c.first + t) * p.gate.row + (size_t)(h * G + rr - t * G) * p.gate.head;
+                    asm volatile("prefetch.global.L2 [%0];\n" ::"l"(line + i % (D / 64) * 64));
                 }
             }
-            // the next unit with slots in the share
-            place += s.tiles + kUnitCost;
-            tile = 0;
-            if (place >= share_hi) return;
-            if (++unit == s.row_tiles * Hkv) {
-                unit = 0;
-                do {
-                    ++b;
-                } while (prefix[b + 1] == prefix[b]);
-                s = load_seq<BM, ST>(p, b, false);
-            }
         }
+        return;
     }
 
     if (warp >= kComputeWarps) {
@@ -434,16 +460,9 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
         // `by` slots on; false past the end of the share
         auto advance = [&](int by) {
             tile += by;
-            while (place + tile < share_hi && tile >= s.tiles) {
+            while (tile >= s.tiles) {
                 tile -= s.tiles;
-                place += s.tiles + kUnitCost;
-                if (++unit == s.row_tiles * Hkv && place + tile < share_hi) {
-                    unit = 0;
-                    do {
-                        ++b;
-                    } while (prefix[b + 1] == prefix[b]);
-                    s = load_seq<BM, ST>(p, b, false);
-                }
+                if (!next_unit()) return false;
             }
             return place + tile < share_hi;
         };
@@ -570,211 +589,219 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
             const int n = done + i, st = n % SLOTS, turn = n / SLOTS;
             // the turn before is over (it may be another group's), so the parity is this turn's
             if (!wait_count(freed + st, turn * Gm::READERS) || !wait(full + st, turn & 1)) return;
-            unsigned char* kt = ring + st * Gm::SLOTB;
-            uint32_t ks = smem_addr(kt);
-            after_wait(ks);
-            const uint32_t vs = ks + HALF;
-            const int pos0 = u.base + (u.tile + i) * ST;
-            const bool whole = pos0 >= all_lo && pos0 + ST <= all_hi;
-            if (pos0 < u.lo || pos0 + ST > kv_len) {
+            unsigned char* slot = ring + st * Gm::SLOTB;
+            uint32_t slot_addr = smem_addr(slot);
+            after_wait(slot_addr);
+            const int slot_pos = u.base + (u.tile + i) * ST;
+            if (slot_pos < u.lo || slot_pos + ST > kv_len) {
                 // values of places outside the sequence become zeros
                 for (int x = lane; x < ST * CPR; x += 32) {
                     const int r = x / CPR;
-                    if (pos0 + r < u.lo || pos0 + r >= kv_len)
-                        *reinterpret_cast<uint4*>(kt + HALF + chunk_at<CPR>(r, x % CPR)) = make_uint4(0, 0, 0, 0);
+                    if (slot_pos + r < u.lo || slot_pos + r >= kv_len)
+                        *reinterpret_cast<uint4*>(slot + HALF + chunk_at<CPR>(r, x % CPR)) = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();  // before the slot is filled again
                 __syncwarp();
             }
-            // with few tokens a slot, even and odd steps go to accumulators of their own (a product waits
-            // for the one before it of the same accumulator)
-            constexpr int SETS = KS <= 2 && !FP8 ? 2 : 1;
-            float S[SETS * KS * 2][4];
+            // in steps of SUB tokens, a loop: unrolled over a slot the code would not stay in the
+            // instruction caches
+#pragma unroll 1
+            for (int sub = 0; sub < ST; sub += SUB) {
+                const int pos0 = slot_pos + sub;
+                if (pos0 >= kv_len || pos0 + SUB <= u.lo) continue;  // nobody's
+                const unsigned char* kt = slot + sub * Gm::ROWB;
+                const uint32_t ks = slot_addr + sub * Gm::ROWB, vs = ks + HALF;
+                const bool whole = pos0 >= all_lo && pos0 + SUB <= all_hi;
+                // with few tokens a slot, even and odd steps go to accumulators of their own (a product waits
+                // for the one before it of the same accumulator)
+                constexpr int SETS = KU <= 2 && !FP8 ? 2 : 1;
+                float S[SETS * KU * 2][4];
 #pragma unroll
-            for (int x = 0; x < SETS * KS * 2; ++x) S[x][0] = S[x][1] = S[x][2] = S[x][3] = 0.0f;
-            if (!FP8) {
+                for (int x = 0; x < SETS * KU * 2; ++x) S[x][0] = S[x][1] = S[x][2] = S[x][3] = 0.0f;
+                if (!FP8) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const int o = SETS == 2 ? (kk & 1) * KS * 2 : 0;
-                    uint32_t a[4];
-                    ldsm4(a, qaddr + (wm * 16 + (lane & 15)) * QP + (kk * 2 + (lane >> 4)) * 16);
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const int o = SETS == 2 ? (kk & 1) * KU * 2 : 0;
+                        uint32_t a[4];
+                        ldsm4(a, qaddr + (wm * 16 + (lane & 15)) * QP + (kk * 2 + (lane >> 4)) * 16);
 #pragma unroll
-                    for (int x = 0; x < KS; ++x) {
-                        uint32_t v[4];
-                        ldsm4(v, ks + chunk_at<CPR>(x * 16 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)));
-                        mma<false>(S[o + 2 * x], a, v[0], v[1]);
-                        mma<false>(S[o + 2 * x + 1], a, v[2], v[3]);
+                        for (int x = 0; x < KU; ++x) {
+                            uint32_t v[4];
+                            ldsm4(v, ks + chunk_at<CPR>(x * 16 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)));
+                            mma<false>(S[o + 2 * x], a, v[0], v[1]);
+                            mma<false>(S[o + 2 * x + 1], a, v[2], v[3]);
+                        }
                     }
-                }
-                if (SETS == 2) {
+                    if (SETS == 2) {
 #pragma unroll
-                    for (int x = 0; x < KS * 2; ++x) {
+                        for (int x = 0; x < KU * 2; ++x) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) S[x][e] += S[(SETS - 1) * KS * 2 + x][e];
+                            for (int e = 0; e < 4; ++e) S[x][e] += S[(SETS - 1) * KU * 2 + x][e];
+                        }
                     }
-                }
-            } else {
-                // a 16-byte chunk is 16 elements of the head: a lane's four bytes are elements 4j..4j+3,
-                // taken as the operand's columns 2j, 2j+1, 2j+8, 2j+9; the queries are read to match
+                } else {
+                    // a 16-byte chunk is 16 elements of the head: a lane's four bytes are elements 4j..4j+3,
+                    // taken as the operand's columns 2j, 2j+1, 2j+8, 2j+9; the queries are read to match
 #pragma unroll
-                for (int kk = 0; kk < D / 16; kk += 2) {
-                    uint32_t a[2][4];
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const uint2 q0 = *reinterpret_cast<const uint2*>(qrow + (wm * 16 + g) * QP + (kk + x) * 32 + j * 8);
-                        const uint2 q1 = *reinterpret_cast<const uint2*>(qrow + (wm * 16 + g + 8) * QP + (kk + x) * 32 + j * 8);
-                        a[x][0] = q0.x;
-                        a[x][1] = q1.x;
-                        a[x][2] = q0.y;
-                        a[x][3] = q1.y;
-                    }
-#pragma unroll
-                    for (int y = 0; y < KS; ++y) {
-                        uint32_t v[4];  // tokens 0-7 and 8-15 of chunk kk, then of chunk kk + 1
-                        ldsm4(v, ks + chunk_at<CPR>(y * 16 + (lane & 15), kk + (lane >> 4)));
+                    for (int kk = 0; kk < D / 16; kk += 2) {
+                        uint32_t a[2][4];
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            mma<true>(S[2 * y], a[x], e4m3_to_half2(v[2 * x], false), e4m3_to_half2(v[2 * x], true));
-                            mma<true>(S[2 * y + 1], a[x], e4m3_to_half2(v[2 * x + 1], false), e4m3_to_half2(v[2 * x + 1], true));
+                            const uint2 q0 = *reinterpret_cast<const uint2*>(qrow + (wm * 16 + g) * QP + (kk + x) * 32 + j * 8);
+                            const uint2 q1 = *reinterpret_cast<const uint2*>(qrow + (wm * 16 + g + 8) * QP + (kk + x) * 32 + j * 8);
+                            a[x][0] = q0.x;
+                            a[x][1] = q1.x;
+                            a[x][2] = q0.y;
+                            a[x][3] = q1.y;
                         }
-                    }
-                }
-            }
-            float mx0 = m[0], mx1 = m[1];
-            if (capped) {
 #pragma unroll
-                for (int x = 0; x < KS * 2; ++x) {
+                        for (int y = 0; y < KU; ++y) {
+                            uint32_t v[4];  // tokens 0-7 and 8-15 of chunk kk, then of chunk kk + 1
+                            ldsm4(v, ks + chunk_at<CPR>(y * 16 + (lane & 15), kk + (lane >> 4)));
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)  // c tanh(y) = c - 2 c / (1 + e^2y)
-                        S[x][e] = fmaf(-2.0f * to_log2, rcp_fast(1.0f + exp2_fast(S[x][e] * (e < 2 ? f0 : f1))), to_log2);
-                }
-            } else {
-#pragma unroll
-                for (int x = 0; x < KS * 2; ++x) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) S[x][e] *= e < 2 ? f0 : f1;
-                }
-            }
-            if (!whole) {
-#pragma unroll
-                for (int x = 0; x < KS * 2; ++x) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int pos = pos0 + x * 8 + 2 * j + (e & 1);
-                        const bool in = e < 2 ? pos < hi0 && pos >= lo0 : pos < hi1 && pos >= lo1;
-                        S[x][e] = in ? S[x][e] : -INFINITY;
-                    }
-                }
-            }
-#pragma unroll
-            for (int x = 0; x < KS * 2; ++x) {
-                mx0 = fmaxf(mx0, fmaxf(S[x][0], S[x][1]));
-                mx1 = fmaxf(mx1, fmaxf(S[x][2], S[x][3]));
-            }
-            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-            const float ref0 = mx0 == -INFINITY ? 0.0f : mx0, ref1 = mx1 == -INFINITY ? 0.0f : mx1;  // nothing seen yet
-            if (__any_sync(0xffffffffu, mx0 != m[0] || mx1 != m[1])) {
-                const float a0 = exp2_fast(m[0] - ref0), a1 = exp2_fast(m[1] - ref1);
-                l[0] *= a0;
-                l[1] *= a1;
-#pragma unroll
-                for (int x = 0; x < ND; ++x) {
-                    O[x][0] *= a0;
-                    O[x][1] *= a0;
-                    O[x][2] *= a1;
-                    O[x][3] *= a1;
-                }
-                m[0] = mx0;
-                m[1] = mx1;
-            }
-#pragma unroll
-            for (int x = 0; x < KS * 2; ++x) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    S[x][e] = exp2_fast(S[x][e] - (e < 2 ? ref0 : ref1));
-                    l[e >> 1] += S[x][e];
-                }
-            }
-
-            // a slot that some rows may not see in full: a value that is not finite must not reach
-            // the rows whose mask leaves it out (0 * inf), so such slots go token by token
-            bool plain = true;
-            if (!whole) {
-                bool bad = false;
-                for (int x = lane; x < ST * CPR; x += 32) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(kt + HALF + x * 16);
-                    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        if (FP8) bad |= (((v[q] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;  // only 0x7f is not finite
-                        else bad |= (v[q] & 0x7f80u) == 0x7f80u || (v[q] & 0x7f800000u) == 0x7f800000u;
-                    }
-                }
-                plain = !__any_sync(0xffffffffu, bad);
-            }
-            if (plain) {
-#pragma unroll
-                for (int x = 0; x < KS; ++x) {
-                    const uint32_t a[4] = {pack2<FP8>(S[2 * x][0], S[2 * x][1]), pack2<FP8>(S[2 * x][2], S[2 * x][3]),
-                                           pack2<FP8>(S[2 * x + 1][0], S[2 * x + 1][1]), pack2<FP8>(S[2 * x + 1][2], S[2 * x + 1][3])};
-                    const int r = x * 16 + (lane & 15);
-                    if (!FP8) {
-#pragma unroll
-                        for (int c = 0; c < ND / 2; ++c) {
-                            uint32_t v[4];
-                            ldsm4t(v, vs + chunk_at<CPR>(r, cs * ND + c * 2 + (lane >> 4)));
-                            mma<false>(O[2 * c], a, v[0], v[1]);
-                            mma<false>(O[2 * c + 1], a, v[2], v[3]);
-                        }
-                    } else {
-                        // a transposed pair of bytes is columns 2n, 2n+1 of one token: tile 2c takes the
-                        // even columns of chunk c, tile 2c + 1 the odd ones
-#pragma unroll
-                        for (int c = 0; c < ND / 2; c += 2) {
-                            uint32_t v[4];
-                            ldsm4t(v, vs + chunk_at<CPR>(r, cs * (ND / 2) + c + (lane >> 4)));
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const uint32_t x0 = e4m3_to_half2(v[2 * y], false), y0 = e4m3_to_half2(v[2 * y], true);
-                                const uint32_t x1 = e4m3_to_half2(v[2 * y + 1], false), y1 = e4m3_to_half2(v[2 * y + 1], true);
-                                mma<true>(O[2 * (c + y)], a, __byte_perm(x0, y0, 0x5410), __byte_perm(x1, y1, 0x5410));
-                                mma<true>(O[2 * (c + y) + 1], a, __byte_perm(x0, y0, 0x7632), __byte_perm(x1, y1, 0x7632));
+                            for (int x = 0; x < 2; ++x) {
+                                mma<true>(S[2 * y], a[x], e4m3_to_half2(v[2 * x], false), e4m3_to_half2(v[2 * x], true));
+                                mma<true>(S[2 * y + 1], a[x], e4m3_to_half2(v[2 * x + 1], false), e4m3_to_half2(v[2 * x + 1], true));
                             }
                         }
                     }
                 }
-            } else {
-#pragma unroll 1
-                for (int t = 0; t < ST; ++t) {
-                    uint32_t b0 = 0, b1 = 0;  // by masks: an index known at run time only would put S into local memory
+                float mx0 = m[0], mx1 = m[1];
+                if (capped) {
 #pragma unroll
-                    for (int x = 0; x < KS * 2; ++x) {
-                        const uint32_t even = x == (t >> 3) && !(t & 1) ? ~0u : 0u, odd = x == (t >> 3) && (t & 1) ? ~0u : 0u;
-                        b0 |= (__float_as_uint(S[x][0]) & even) | (__float_as_uint(S[x][1]) & odd);
-                        b1 |= (__float_as_uint(S[x][2]) & even) | (__float_as_uint(S[x][3]) & odd);
+                    for (int x = 0; x < KU * 2; ++x) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)  // c tanh(y) = c - 2 c / (1 + e^2y)
+                            S[x][e] = fmaf(-2.0f * to_log2, rcp_fast(1.0f + exp2_fast(S[x][e] * (e < 2 ? f0 : f1))), to_log2);
                     }
-                    const float p0 = __uint_as_float(__shfl_sync(0xffffffffu, b0, (lane & ~3) | ((t >> 1) & 3)));
-                    const float p1 = __uint_as_float(__shfl_sync(0xffffffffu, b1, (lane & ~3) | ((t >> 1) & 3)));
-                    const int pos = pos0 + t;
-                    const bool in0 = pos < hi0 && pos >= lo0, in1 = pos < hi1 && pos >= lo1;
+                } else {
+#pragma unroll
+                    for (int x = 0; x < KU * 2; ++x) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) S[x][e] *= e < 2 ? f0 : f1;
+                    }
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int x = 0; x < KU * 2; ++x) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int pos = pos0 + x * 8 + 2 * j + (e & 1);
+                            const bool in = e < 2 ? pos < hi0 && pos >= lo0 : pos < hi1 && pos >= lo1;
+                            S[x][e] = in ? S[x][e] : -INFINITY;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < KU * 2; ++x) {
+                    mx0 = fmaxf(mx0, fmaxf(S[x][0], S[x][1]));
+                    mx1 = fmaxf(mx1, fmaxf(S[x][2], S[x][3]));
+                }
+                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
+                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
+                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
+                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+                const float ref0 = mx0 == -INFINITY ? 0.0f : mx0, ref1 = mx1 == -INFINITY ? 0.0f : mx1;  // nothing seen yet
+                if (__any_sync(0xffffffffu, mx0 != m[0] || mx1 != m[1])) {
+                    const float a0 = exp2_fast(m[0] - ref0), a1 = exp2_fast(m[1] - ref1);
+                    l[0] *= a0;
+                    l[1] *= a1;
 #pragma unroll
                     for (int x = 0; x < ND; ++x) {
+                        O[x][0] *= a0;
+                        O[x][1] *= a0;
+                        O[x][2] *= a1;
+                        O[x][3] *= a1;
+                    }
+                    m[0] = mx0;
+                    m[1] = mx1;
+                }
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float v;
-                            if (!FP8) {
-                                const int col = cs * (ND * 8) + x * 8 + 2 * j + e;
-                                v = bf16_bits_to_float(*reinterpret_cast<const uint16_t*>(kt + HALF + chunk_at<CPR>(t, col >> 3) + (col & 7) * 2));
-                            } else {
-                                const int col = cs * (ND * 8) + (x >> 1) * 16 + 4 * j + 2 * e + (x & 1);
-                                const uint32_t hh = e4m3_to_half2(*(kt + HALF + chunk_at<CPR>(t, col >> 4) + (col & 15)), false);
-                                v = __low2float(*reinterpret_cast<const __half2*>(&hh));
+                for (int x = 0; x < KU * 2; ++x) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        S[x][e] = exp2_fast(S[x][e] - (e < 2 ? ref0 : ref1));
+                        l[e >> 1] += S[x][e];
+                    }
+                }
+
+                // a slot that some rows may not see in full: a value that is not finite must not reach
+                // the rows whose mask leaves it out (0 * inf), so such slots go token by token
+                bool plain = true;
+                if (!whole) {
+                    bool bad = false;
+                    for (int x = lane; x < SUB * CPR; x += 32) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(kt + HALF + x * 16);
+                        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            if (FP8) bad |= (((v[q] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;  // only 0x7f is not finite
+                            else bad |= (v[q] & 0x7f80u) == 0x7f80u || (v[q] & 0x7f800000u) == 0x7f800000u;
+                        }
+                    }
+                    plain = !__any_sync(0xffffffffu, bad);
+                }
+                if (plain) {
+#pragma unroll
+                    for (int x = 0; x < KU; ++x) {
+                        const uint32_t a[4] = {pack2<FP8>(S[2 * x][0], S[2 * x][1]), pack2<FP8>(S[2 * x][2], S[2 * x][3]),
+                                               pack2<FP8>(S[2 * x + 1][0], S[2 * x + 1][1]), pack2<FP8>(S[2 * x + 1][2], S[2 * x + 1][3])};
+                        const int r = x * 16 + (lane & 15);
+                        if (!FP8) {
+#pragma unroll
+                            for (int c = 0; c < ND / 2; ++c) {
+                                uint32_t v[4];
+                                ldsm4t(v, vs + chunk_at<CPR>(r, cs * ND + c * 2 + (lane >> 4)));
+                                mma<false>(O[2 * c], a, v[0], v[1]);
+                                mma<false>(O[2 * c + 1], a, v[2], v[3]);
                             }
-                            if (in0) O[x][e] = fmaf(p0, v, O[x][e]);
-                            if (in1) O[x][e + 2] = fmaf(p1, v, O[x][e + 2]);
+                        } else {
+                            // a transposed pair of bytes is columns 2n, 2n+1 of one token: tile 2c takes the
+                            // even columns of chunk c, tile 2c + 1 the odd ones
+#pragma unroll
+                            for (int c = 0; c < ND / 2; c += 2) {
+                                uint32_t v[4];
+                                ldsm4t(v, vs + chunk_at<CPR>(r, cs * (ND / 2) + c + (lane >> 4)));
+#pragma unroll
+                                for (int y = 0; y < 2; ++y) {
+                                    const uint32_t x0 = e4m3_to_half2(v[2 * y], false), y0 = e4m3_to_half2(v[2 * y], true);
+                                    const uint32_t x1 = e4m3_to_half2(v[2 * y + 1], false), y1 = e4m3_to_half2(v[2 * y + 1], true);
+                                    mma<true>(O[2 * (c + y)], a, __byte_perm(x0, y0, 0x5410), __byte_perm(x1, y1, 0x5410));
+                                    mma<true>(O[2 * (c + y) + 1], a, __byte_perm(x0, y0, 0x7632), __byte_perm(x1, y1, 0x7632));
+                                }
+                            }
+                        }
+                    }
+                } else {
+#pragma unroll 1
+                    for (int t = 0; t < SUB; ++t) {
+                        uint32_t b0 = 0, b1 = 0;  // by masks: an index known at run time only would put S into local memory
+#pragma unroll
+                        for (int x = 0; x < KU * 2; ++x) {
+                            const uint32_t even = x == (t >> 3) && !(t & 1) ? ~0u : 0u, odd = x == (t >> 3) && (t & 1) ? ~0u : 0u;
+                            b0 |= (__float_as_uint(S[x][0]) & even) | (__float_as_uint(S[x][1]) & odd);
+                            b1 |= (__float_as_uint(S[x][2]) & even) | (__float_as_uint(S[x][3]) & odd);
+                        }
+                        const float p0 = __uint_as_float(__shfl_sync(0xffffffffu, b0, (lane & ~3) | ((t >> 1) & 3)));
+                        const float p1 = __uint_as_float(__shfl_sync(0xffffffffu, b1, (lane & ~3) | ((t >> 1) & 3)));
+                        const int pos = pos0 + t;
+                        const bool in0 = pos < hi0 && pos >= lo0, in1 = pos < hi1 && pos >= lo1;
+#pragma unroll
+                        for (int x = 0; x < ND; ++x) {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float v;
+                                if (!FP8) {
+                                    const int col = cs * (ND * 8) + x * 8 + 2 * j + e;
+                                    v = bf16_bits_to_float(*reinterpret_cast<const uint16_t*>(kt + HALF + chunk_at<CPR>(t, col >> 3) + (col & 7) * 2));
+                                } else {
+                                    const int col = cs * (ND * 8) + (x >> 1) * 16 + 4 * j + 2 * e + (x & 1);
+                                    const uint32_t hh = e4m3_to_half2(*(kt + HALF + chunk_at<CPR>(t, col >> 4) + (col & 15)), false);
+                                    v = __low2float(*reinterpret_cast<const __half2*>(&hh));
+                                }
+                                if (in0) O[x][e] = fmaf(p0, v, O[x][e]);
+                                if (in1) O[x][e + 2] = fmaf(p1, v, O[x][e + 2]);
+                            }
                         }
                     }
                 }
