@@ -176,7 +176,8 @@ gdn_status gdn_attn_decode(const gdn_attn_config* cfg, const gdn_kv_cache* cache
         misaligned(workspace, 16))
         return GDN_ERR_MISALIGNED;
     // the kernel numbers its work units (token tiles of a row tile of a head) in 32 bits
-    const int rows = T * a.sh.G, tt = gdn::attn_token_tile(a.sh.d, a.sh.fp8, rows), rt = gdn::attn_row_tile(a.sh.d, a.sh.fp8, rows);
+    const int rows = T * a.sh.G, tt = gdn::attn_token_tile(a.sh.d, a.sh.fp8, a.sh.page_size, rows),
+              rt = gdn::attn_row_tile(a.sh.d, a.sh.fp8, a.sh.page_size, rows);
     const double tiles = (double)B * (ceil((double)a.c.max_pages * a.sh.page_size / tt) + 8) * a.sh.Hkv * ((rows + rt - 1) / rt);
     if (tiles > 2.0e9) return GDN_ERR_UNSUPPORTED;
     a.B = B;
@@ -189,14 +190,15 @@ gdn_status gdn_attn_decode(const gdn_attn_config* cfg, const gdn_kv_cache* cache
     a.err_flag = err_flag;
     a.counters = static_cast<unsigned int*>(workspace);
     a.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + gdn::kAttnCounters * sizeof(unsigned int));
-    return from_cuda(gdn::launch_attn_decode(a, (cudaStream_t)stream));
+    return from_cuda(gdn::attn_rows_supported(a.sh.fp8, a.sh.page_size, rows) ? gdn::launch_attn_rows(a, (cudaStream_t)stream)
+                                                                              : gdn::launch_attn_decode(a, (cudaStream_t)stream));
 }
 
 size_t gdn_attn_decode_workspace_bytes(const gdn_attn_config* cfg, int32_t B, int32_t T) {
     gdn::AttnShape sh;
     if (check_attn_config(cfg, &sh) != GDN_OK) return 0;
     if (B < 0 || B > gdn::kAttnMaxBatch || T <= 0 || T > gdn::kMaxTokens) return 0;
-    return gdn::attn_workspace_bytes(sh.d, sh.fp8, T * sh.G);
+    return gdn::attn_workspace_bytes(sh.d, sh.fp8, sh.page_size, T * sh.G);
 }
 
 gdn_status gdn_rope_inv_freq_host(int32_t rotary_dim, double theta, double factor, int32_t yarn, int32_t original_len,

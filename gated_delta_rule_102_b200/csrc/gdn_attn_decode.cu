@@ -30,26 +30,21 @@
 //
 // Bound by HBM for few query rows: 2 G n flop for each byte of a bf16 cache (8 query heads
 // per key/value head, one token: 8 flop per byte). Every wait is bounded.
-#include <cuda.h>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include <mutex>
 
 #include "gdn_attn.h"
-#include "gdn_device.cuh"
-#include "gdn_internal.h"
+#include "gdn_attn_device.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kLoadWarps = 3, kComputeWarps = 8, kAttnThreads = (kLoadWarps + 1 + kComputeWarps) * 32;
 constexpr int kLaunchRegs = 168;
 #ifndef GDN_ATTN_UNIT_COST
-#define GDN_ATTN_UNIT_COST 14
+#define GDN_ATTN_UNIT_COST 12
 #endif
 #ifndef GDN_ATTN_KU
 #define GDN_ATTN_KU 2
@@ -58,7 +53,7 @@ constexpr int kLaunchRegs = 168;
 #define GDN_ATTN_NQ 6
 #endif
 #ifndef GDN_ATTN_SHORT_COST
-#define GDN_ATTN_SHORT_COST 4
+#define GDN_ATTN_SHORT_COST 6
 #endif
 #ifndef GDN_ATTN_SINGLE
 #define GDN_ATTN_SINGLE 4
@@ -67,7 +62,7 @@ constexpr int kLaunchRegs = 168;
 #define GDN_ATTN_MIN_SHARE 8
 #endif
 constexpr int kShortCost = GDN_ATTN_SHORT_COST, kUnitCost = GDN_ATTN_UNIT_COST;  // what a unit costs beside its slots, in slots (its queries, the join, the output)
-constexpr int kJoinFlat = 12, kJoinGroup = 8;  // pieces of a unit that one CTA joins at once, and groups of more
+constexpr int kMinShare = GDN_ATTN_MIN_SHARE;  // places of a CTA at least: fewer CTAs, and joins, for little work
 constexpr int kSingle = GDN_ATTN_SINGLE;    // a piece of so many slots or fewer is one token group's alone
 
 // Geometry: D head size, WM row groups of 16 query rows.
@@ -92,160 +87,6 @@ struct Geo {
     static constexpr int SLOTS = FIT > 12 ? 12 : FIT;
     static_assert(SLOTS >= 8 && ST % SUB == 0 && NG >= 1, "ring");
 };
-
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
-    const int n = valid ? 16 : 0;  // 0: the 16 bytes are filled with zeros and nothing is read
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
-__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int c3, int c4, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3, "
-        "%4}], [%5];\n" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(c3), "r"(c4), "r"(bar)
-        : "memory");
-}
-// The matrix loads are not volatile, so that the compiler may move them between the products;
-// what keeps them behind the wait for their data and before its release is after_wait() on the
-// address that they use and before_release() on the accumulators that depend on them.
-__device__ __forceinline__ void after_wait(uint32_t& addr) { asm volatile("" : "+r"(addr)::"memory"); }
-template <int N>
-__device__ __forceinline__ void before_release(float (&acc)[N][4]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        asm volatile("" : "+f"(acc[i][0]), "+f"(acc[i][1]), "+f"(acc[i][2]), "+f"(acc[i][3])::"memory");
-}
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-    asm("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
-}
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
-    asm("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];\n"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
-}
-// c += a b, 16x8x16, bf16 or fp16 operands (both the same), fp32 sums.
-template <bool HALF>
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    if (HALF)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
-            "%2, %3};\n"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, "
-            "%1, %2, %3};\n"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// Two e4m3 bytes (the low or high half of w) as two fp16, exactly.
-__device__ __forceinline__ uint32_t e4m3_to_half2(uint32_t w, bool high) {
-    uint32_t r;
-    const uint16_t h = (uint16_t)(high ? w >> 16 : w);
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(h));
-    return r;
-}
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float rcp_fast(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-template <bool HALF>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    if (HALF) {
-        const __half2 h = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// Byte offset of 16-byte chunk c of token row r in a slot's keys (or values): atoms of eight
-// rows by 128 bytes in which chunk c is stored at c ^ (r % 8) (64-byte rows: two to a line,
-// c ^ (r / 2 % 4)), the swizzles that the TMA unit applies. Eight rows, eight bank groups.
-template <int CPR>
-__device__ __forceinline__ int chunk_at(int r, int c) {
-    if (CPR >= 8) return ((r >> 3) * (CPR / 8) + (c >> 3)) * 1024 + (r & 7) * 128 + (((c ^ r) & 7) << 4);
-    return r * 64 + (((c ^ (r >> 1)) & 3) << 4);
-}
-
-// A sequence as the schedule sees it.
-struct Seq {
-    int n, first, past, slot;  // tokens of this call, their first row, tokens before them
-    int lo, base, tiles;       // first position any row attends, the slots' first position, slots
-    int cost;                  // places of a unit in the schedule beside its slots'
-    int row_tiles;
-};
-
-template <int BM, int ST>
-__device__ __forceinline__ Seq load_seq(const AttnArgs& p, int b, bool report) {
-    Seq s;
-    s.tiles = 0;
-    s.cost = 0;
-    s.row_tiles = 0;
-    s.slot = __ldg(p.slots + b);
-    s.first = b * p.T;
-    s.n = p.T;
-    if (p.cu) {
-        s.first = __ldg(p.cu + b);
-        s.n = __ldg(p.cu + b + 1) - s.first;
-    }
-    s.past = 0;
-    s.lo = 0;
-    s.base = 0;
-    if (s.n < 0 || s.n > p.T || s.first < 0 || s.first > p.total - s.n) {
-        if (report && p.err_flag) atomicOr(p.err_flag, GDN_DEVICE_ERR_SEQLEN_BIT);
-        s.n = 0;
-        return s;
-    }
-    if (s.n == 0) return s;
-    if (s.slot < 0 || s.slot >= p.c.rows) {
-        if (report && p.err_flag) atomicOr(p.err_flag, GDN_DEVICE_ERR_SLOT_RANGE_BIT);
-        return s;
-    }
-    s.past = __ldg(p.c.seq_lens + s.slot);
-    if (s.past < 0 || s.past > p.c.max_pages * p.sh.page_size - s.n) {
-        if (report && p.err_flag) atomicOr(p.err_flag, GDN_DEVICE_ERR_SEQLEN_BIT);
-        return s;
-    }
-    if (p.sh.window > 0 && s.past + 1 > p.sh.window) s.lo = s.past + 1 - p.sh.window;
-    s.base = s.lo & ~(ST - 1);
-    s.tiles = (s.past + s.n - s.base + ST - 1) / ST;
-    s.cost = s.tiles <= kSingle ? kShortCost : kUnitCost;
-    s.row_tiles = (s.n * p.sh.G + BM - 1) / BM;
-    return s;
-}
-
-// A CTA's piece of a unit, as the loading warps describe it to the computing ones.
-struct Piece {
-    int n, first, past, lo, base;  // of the sequence
-    int h, rt;                     // key/value head, row tile
-    int tile, count;               // its first slot and how many
-    int last;                      // the share ends with it
-    int c0, c1;                    // the CTAs that share the unit
-};
-
-__device__ __forceinline__ int load_acquire(const int* at) {
-    int v;
-    asm volatile("ld.acquire.cta.shared::cta.b32 %0, [%1];\n" : "=r"(v) : "r"(smem_addr(at)) : "memory");
-    return v;
-}
-__device__ __forceinline__ void add_release(int* at) {
-    asm volatile("red.release.cta.shared::cta.add.u32 [%0], 1;\n" ::"r"(smem_addr(at)) : "memory");
-}
-__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + exp2_fast(-x * kLog2e)); }
-
-// Raises the call's timeout flag and makes every role of the CTA leave at its next wait.
-__device__ __noinline__ void attn_abort(int32_t* err_flag, volatile int* stop) {
-    if (err_flag) atomicOr(err_flag, GDN_DEVICE_ERR_TIMEOUT_BIT);
-    *stop = 1;
-}
 
 template <int D, bool FP8, int WM>
 __global__ void __launch_bounds__(kAttnThreads, 1)
@@ -272,7 +113,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
     int* prefix = misc + 16;                                      // [B + 1] cost of the sequences before each
     volatile int* stop = misc + 15;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int Hkv = p.sh.Hkv, G = p.sh.G, ps = p.sh.page_size;
+    const int Hkv = p.sh.Hkv, G = p.sh.G;
 
     if (tid == 0) {
         for (int i = 0; i < SLOTS; ++i) {
@@ -291,74 +132,10 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
-    // ---- the schedule: the cost of every sequence, summed ----
-    int total = 0;
-    for (int base = 0; base < p.B; base += kAttnThreads) {
-        const int b = base + tid;
-        int t = 0;
-        if (b < p.B) {
-            const Seq s = load_seq<BM, ST>(p, b, blockIdx.x == 0);
-            t = (s.tiles + s.cost) * s.row_tiles * Hkv;
-        }
-        int x = t;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        if (lane == 31) misc[warp] = x;
-        __syncthreads();
-        int before = total, sum = 0;
-#pragma unroll
-        for (int w = 0; w < kAttnThreads / 32; ++w) {
-            if (w < warp) before += misc[w];
-            sum += misc[w];
-        }
-        if (b < p.B) prefix[b] = before + x - t;
-        total += sum;
-        __syncthreads();
-    }
-    if (tid == 0) prefix[p.B] = total;
-    __syncthreads();
-    // As many CTAs as there are SMs, but no fewer slots a CTA than token groups. CTA c has the
-    // places c * per + min(c, more) on: per of them, one more for the first ones. A unit takes
-    // some places that no slot stands for (what it costs beside its slots) and one for each slot.
-    const int ctas = min((int)gridDim.x, (total + GDN_ATTN_MIN_SHARE - 1) / GDN_ATTN_MIN_SHARE);
-    if ((int)blockIdx.x >= ctas) return;
-    const int per = total / ctas, more = total - per * ctas;
-    const int share_lo = blockIdx.x * per + min((int)blockIdx.x, more), share_hi = share_lo + per + ((int)blockIdx.x < more);
-    auto cta_of = [&](int place) {
-        const int big = more * (per + 1);
-        return place < big ? place / (per + 1) : more + (place - big) / per;
-    };
-    int b = 0;
-    {
-        int hi = p.B;
-        while (hi - b > 1) {
-            const int mid = (b + hi) >> 1;
-            if (prefix[mid] <= share_lo) b = mid; else hi = mid;
-        }
-    }
-    Seq s = load_seq<BM, ST>(p, b, false);  // the last sequence that starts at or before the share: it has units
-    int unit = (share_lo - prefix[b]) / (s.tiles + s.cost);  // row_tile * Hkv + kv head
-    int place = prefix[b] + unit * (s.tiles + s.cost) + s.cost;  // of the unit's first slot
-    int tile = max(share_lo - place, 0);
-    if (place + tile >= share_hi) return;  // nothing but a unit's overhead
+    Share<BM, ST, kSingle, kShortCost, kUnitCost> at(p, prefix);
+    at.template sum_batch<kAttnThreads>(prefix, misc);
+    if (!at.begin(kMinShare)) return;
 
-    // to the next unit; false when its slots lie past the share
-    auto next_unit = [&] {
-        place += s.tiles;  // the unit's end
-        if (place >= share_hi) return false;
-        if (++unit == s.row_tiles * Hkv) {
-            unit = 0;
-            do {
-                ++b;
-            } while (prefix[b + 1] == prefix[b]);
-            s = load_seq<BM, ST>(p, b, false);
-        }
-        place += s.cost;
-        return place < share_hi;
-    };
     auto give_up = [&] { return *stop != 0; };
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (mbar_wait_deadline(bar, parity, kWaitTimeoutCycles, give_up)) return true;
@@ -388,10 +165,10 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
         // ================= queries =================
         bool more_units = true;
         for (int ord = 0; more_units; ++ord) {
-            const Seq c = s;
-            const int rt = unit / Hkv, h = unit - rt * Hkv, at = place, from = tile;
-            more_units = next_unit();  // before this one is described: it may be the last
-            tile = 0;
+            const Seq c = at.s;
+            const int rt = at.unit / Hkv, h = at.unit - rt * Hkv, place = at.place, from = at.tile;
+            more_units = at.next_unit();  // before this one is described: it may be the last
+            at.tile = 0;
             // the unit's queries: row r is token r / G, query head h * G + r % G; rows past the last
             // are left as they are (a row's products touch no other row)
             const int qs = ord % NQ, rows = min(BM, c.n * G - rt * BM);
@@ -399,8 +176,8 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
             if (!wait_count(qfreed + qs, ord / NQ * kComputeWarps)) return;
             unsigned char* q = qbuf + qs * QB;
             if (lane == 0) {
-                pieces[qs] = Piece{c.n, c.first, c.past, c.lo, c.base, h, rt, from, min(c.tiles - from, share_hi - at - from),
-                                   !more_units, cta_of(at), cta_of(at + c.tiles - 1)};
+                pieces[qs] = Piece{c.n, c.first, c.past, c.lo, c.base, h, rt, from, min(c.tiles - from, at.hi - place - from),
+                                   !more_units, at.cta_of(place), at.cta_of(place + c.tiles - 1)};
                 if (!FP8) mbar_arrive_expect_tx(qfull + qs, rows * D * 2);
             }
             __syncwarp();
@@ -457,53 +234,35 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
     if (warp >= kComputeWarps) {
         // ================= loading =================
         const int pw = warp - kComputeWarps;
-        // `by` slots on; false past the end of the share
-        auto advance = [&](int by) {
-            tile += by;
-            while (tile >= s.tiles) {
-                tile -= s.tiles;
-                if (!next_unit()) return false;
-            }
-            return place + tile < share_hi;
-        };
         const size_t token_stride = (size_t)Hkv * Gm::ROWB;
         // With TMA, lane x (16 + x) fetches chunk x of the slot's keys (values), `box` tokens of
         // one page; otherwise a lane looks tokens up for everybody.
         constexpr int LOOK = (ST + 31) / 32;
         int tok[LOOK];  // token numbers (page * page_size + offset), -1: none
-        auto look_up = [&](int pos, int len) {
-            if (pos + len <= s.lo || pos >= s.past + s.n) return -1;
-            const int pg = pos / ps;
-            const int page = __ldg(p.c.table + (size_t)s.slot * p.c.max_pages + pg);
-            if (page >= 0 && page < p.c.num_pages) return page * ps + (pos - pg * ps);
-            if (p.err_flag) atomicOr(p.err_flag, GDN_DEVICE_ERR_PAGE_BIT);
-            return -1;
-        };
         auto find_tokens = [&] {
-            const int pos0 = s.base + tile * ST;
+            const int pos0 = at.s.base + at.tile * ST;
             if (box) {
                 const int x = lane & 15;
-                tok[0] = x * box < ST ? look_up(pos0 + x * box, box) : -1;
+                tok[0] = x * box < ST ? at.look_up(pos0 + x * box, box) : -1;
             } else {
 #pragma unroll
-                for (int i = 0; i < LOOK; ++i) tok[i] = i * 32 + lane < ST ? look_up(pos0 + i * 32 + lane, 1) : -1;
+                for (int i = 0; i < LOOK; ++i) tok[i] = i * 32 + lane < ST ? at.look_up(pos0 + i * 32 + lane, 1) : -1;
             }
         };
         constexpr int RPP = 32 / CPR;  // token rows of one warp-wide copy
         const int chunk = lane % CPR, sub = lane / CPR;
-        bool more_slots = pw == 0 || advance(pw);
+        bool more_slots = pw == 0 || at.advance(pw);
         if (more_slots) find_tokens();
         for (int i = pw; more_slots; i += kLoadWarps) {
-            const int rt = unit / Hkv, h = unit - rt * Hkv;
-            const int st = i % SLOTS, turn = i / SLOTS;
+            const int h = at.unit % Hkv, st = i % SLOTS, turn = i / SLOTS;
             if (!wait_count(freed + st, turn * Gm::READERS)) break;
-            const uint32_t at = smem_addr(ring + st * Gm::SLOTB);
+            const uint32_t dst = smem_addr(ring + st * Gm::SLOTB);
             if (box) {
                 const unsigned got = __ballot_sync(0xffffffffu, tok[0] >= 0);
                 if (lane == 0) mbar_arrive_expect_tx(full + st, __popc(got) * box * Gm::ROWB);
                 __syncwarp();
                 if (tok[0] >= 0)
-                    tma_load_5d(at + (lane >> 4) * HALF + (lane & 15) * box * Gm::ROWB, lane < 16 ? &map_k : &map_v, tok[0] >> 3, h,
+                    tma_load_5d(dst + (lane >> 4) * HALF + (lane & 15) * box * Gm::ROWB, lane < 16 ? &map_k : &map_v, tok[0] >> 3, h,
                                 smem_addr(full + st));
             } else {
                 const unsigned char* kb = static_cast<const unsigned char*>(p.c.k) + (size_t)h * Gm::ROWB + chunk * 16;
@@ -522,14 +281,14 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
                         const size_t off = t[x] < 0 ? 0 : (size_t)t[x] * token_stride;
-                        const uint32_t to = at + chunk_at<CPR>((k + x) * RPP + sub, chunk);
+                        const uint32_t to = dst + chunk_at<CPR>((k + x) * RPP + sub, chunk);
                         cp16(to, kb + off, t[x] >= 0);
                         cp16(to + HALF, vb + off, t[x] >= 0);
                     }
                 }
                 cp_async_arrive(full + st);
             }
-            more_slots = advance(kLoadWarps);
+            more_slots = at.advance(kLoadWarps);
             if (more_slots) find_tokens();
         }
         cp_wait_all();
@@ -946,121 +705,8 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
         }
     }
 
-    // ---- units over several CTAs: the last of them to get here joins the pieces, in their order ----
-    // More than kJoinFlat pieces are joined in groups of kJoinGroup first (by the last CTA of the
-    // group, into its first piece's place), then the groups: at 74 pieces of 8 KB one CTA alone
-    // would read 600 KB.
-    if (!split_first && !split_last) return;
-    __threadfence();
-    if (!meet()) return;
-    float* wt = reinterpret_cast<float*>(ring);  // [BM][WP] weights of the pieces, their sum and maximum
-    constexpr int WP = kAttnMaxCtas + 2;
-    static_assert(BM * WP * 4 <= SLOTS * Gm::SLOTB, "weights");
-    for (int which = 0; which < 2; ++which) {
-        if (!(which ? split_last : split_first)) continue;
-        const Piece u = pieces[NQ + which];
-        const int rows = min(BM, u.n * G - u.rt * BM), all = u.c1 - u.c0 + 1;
-        auto place_of = [&](int i) { return p.partial + (size_t)((u.c0 + i) * 2 + (i == 0)) * PSTRIDE; };
-        const bool flat = all <= kJoinFlat;
-        for (int level = flat ? 1 : 0; level < 2; ++level) {
-            // level 0: this CTA's group of pieces; level 1: all pieces, or the groups' first places
-            const int step = level == 1 && !flat ? kJoinGroup : 1;
-            const int from = level == 0 ? ((int)blockIdx.x - u.c0) / kJoinGroup * kJoinGroup : 0;
-            const int count = level == 0 ? min(kJoinGroup, all - from) : (all + step - 1) / step;
-            unsigned int* counter = p.counters + (level == 1 ? u.c0 : kAttnMaxCtas + (u.c0 + from) * 2 + (from == 0));
-            if (tid == 0) misc[12] = atomicAdd(counter, 1u) == (unsigned)(count - 1);
-            if (!meet()) return;
-            if (!misc[12]) break;  // (written next after another meeting)
-            __threadfence();
-            auto part = [&](int i) -> const float* { return place_of(from + i * step); };
-            for (int r = warp; r < rows; r += kComputeWarps) {
-                float* w = wt + r * WP;
-                float top = -INFINITY, tot = 0.0f;
-                for (int i = lane; i < count; i += 32) {
-                    w[i] = __ldcg(part(i) + BM * D + r);
-                    top = fmaxf(top, w[i]);
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                for (int i = lane; i < count; i += 32) {
-                    w[i] = w[i] == -INFINITY ? 0.0f : exp2_fast(w[i] - top);
-                    tot = fmaf(w[i], __ldcg(part(i) + BM * D + BM + r), tot);
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-                if (lane == 0) {
-                    w[kAttnMaxCtas] = tot;
-                    w[kAttnMaxCtas + 1] = top;
-                }
-            }
-            if (!meet()) return;
-            for (int k = tid; k < rows * (D / 4); k += kComputeWarps * 32) {
-                const int r = k / (D / 4), col = (k % (D / 4)) * 4;
-                const float* w = wt + r * WP;
-                const float* src = part(0) + r * D + col;
-                const float* rest = count > 1 ? part(1) + r * D + col : src;
-                const size_t stride = (size_t)step * 2 * PSTRIDE;
-                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                for (int i0 = 0; i0 < count; i0 += 10) {
-                    float4 x[10];
-#pragma unroll
-                    for (int i = 0; i < 10; ++i) {
-                        const float* at = i0 + i == 0 ? src : rest + (size_t)(i0 + i - 1) * stride;
-                        x[i] = i0 + i < count ? __ldcg(reinterpret_cast<const float4*>(at)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 10; ++i) {
-                        const float f = i0 + i < count ? w[i0 + i] : 0.0f;
-                        o.x = fmaf(f, x[i].x, o.x);
-                        o.y = fmaf(f, x[i].y, o.y);
-                        o.z = fmaf(f, x[i].z, o.z);
-                        o.w = fmaf(f, x[i].w, o.w);
-                    }
-                }
-                if (level == 0) {
-                    *reinterpret_cast<float4*>(place_of(from) + r * D + col) = o;
-                    continue;
-                }
-                const int rr = u.rt * BM + r, t = rr / G, head = u.h * G + rr - t * G;
-                const size_t row = (size_t)u.first + t, at = row * p.sh.Hq + head;
-                const float inv = p.sh.v_scale / w[kAttnMaxCtas];
-                o.x *= inv;
-                o.y *= inv;
-                o.z *= inv;
-                o.w *= inv;
-                if (p.gate.ptr) {
-                    const uint2 z = __ldg(reinterpret_cast<const uint2*>(p.gate.ptr + row * p.gate.row + (size_t)head * p.gate.head + col));
-                    o.x *= sigmoid_fast(__uint_as_float(z.x << 16));
-                    o.y *= sigmoid_fast(__uint_as_float(z.x & 0xffff0000u));
-                    o.z *= sigmoid_fast(__uint_as_float(z.y << 16));
-                    o.w *= sigmoid_fast(__uint_as_float(z.y & 0xffff0000u));
-                }
-                *reinterpret_cast<uint2*>(p.out + at * D + col) = make_uint2(pack2<false>(o.x, o.y), pack2<false>(o.z, o.w));
-                if (p.lse && col == 0) p.lse[at] = (w[kAttnMaxCtas + 1] + log2f(w[kAttnMaxCtas])) * kLn2;
-            }
-            if (tid == 0) *counter = 0;
-            if (level == 0 && tid < rows) {  // the group's maximum and sum, in place of its first piece's
-                float* to = place_of(from) + BM * D;
-                to[tid] = wt[tid * WP + kAttnMaxCtas + 1];
-                to[BM + tid] = wt[tid * WP + kAttnMaxCtas];
-            }
-            if (level == 0) __threadfence();
-            if (!meet()) return;  // the next weights go where these are
-        }
-        if (which == 0 && split_last && !meet()) return;  // misc[12] is written again
-    }
-}
-
-// A tensor map over a pool of pages as [head][token / 8][128-byte block][token % 8][byte],
-// in boxes of `box` tokens of one head: the atoms that the kernels read, in their order.
-bool make_pool_map(CUtensorMap* m, void* pool, const AttnArgs& a, int row_bytes, int box) {
-    const int inner = row_bytes < 128 ? row_bytes : 128, blocks = row_bytes / inner, esz = a.sh.fp8 ? 1 : 2;
-    const cuuint64_t token = (cuuint64_t)a.sh.Hkv * row_bytes;
-    const cuuint64_t dims[5] = {(cuuint64_t)(inner / esz), 8, (cuuint64_t)blocks, (cuuint64_t)a.c.num_pages * a.sh.page_size / 8,
-                                (cuuint64_t)a.sh.Hkv};
-    const cuuint64_t strides[4] = {token, (cuuint64_t)inner, token * 8, (cuuint64_t)row_bytes};
-    const cuuint32_t boxes[5] = {(cuuint32_t)(inner / esz), 8, (cuuint32_t)blocks, (cuuint32_t)box / 8, 1};
-    return encode_tensor_map(m, a.sh.fp8, 5, pool, dims, strides, boxes, inner);
+    static_assert(BM * (kAttnMaxCtas + 2) * 4 <= SLOTS * Gm::SLOTB, "weights");
+    join_units<D, BM, kComputeWarps * 32>(p, pieces + NQ, split_first, split_last, reinterpret_cast<float*>(ring), misc + 12, meet);
 }
 
 template <int D, bool FP8, int WM>
@@ -1132,14 +778,17 @@ cudaError_t launch_rows(const AttnArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-int attn_row_tile(int d, bool fp8, int rows) {
+int attn_row_tile(int d, bool fp8, int page_size, int rows) {
+    if (attn_rows_supported(fp8, page_size, rows)) return 128;
     return with_geometry(d, fp8, rows, [](auto g) { return decltype(g)::BM; });
 }
-int attn_token_tile(int d, bool fp8, int rows) {
+int attn_token_tile(int d, bool fp8, int page_size, int rows) {
+    if (attn_rows_supported(fp8, page_size, rows)) return 64;
     return with_geometry(d, fp8, rows, [](auto g) { return decltype(g)::ST; });
 }
-size_t attn_workspace_bytes(int d, bool fp8, int rows) {
-    return kAttnCounters * sizeof(unsigned int) + (size_t)kAttnMaxCtas * 2 * attn_row_tile(d, fp8, rows) * (d + 2) * sizeof(float);
+size_t attn_workspace_bytes(int d, bool fp8, int page_size, int rows) {
+    return kAttnCounters * sizeof(unsigned int) +
+           (size_t)kAttnMaxCtas * 2 * attn_row_tile(d, fp8, page_size, rows) * (d + 2) * sizeof(float);
 }
 
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t stream) {

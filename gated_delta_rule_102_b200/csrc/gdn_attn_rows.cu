@@ -1,0 +1,498 @@
+// Attention of many query rows per key/value head (several new tokens of a sequence, as in
+// the verification of a draft) over a paged bf16 cache, on the fifth-generation tensor
+// cores: the same result, schedule and workspace as the kernel for few rows, which its
+// matrix instructions hold back beyond 16 rows.
+//
+//   S = Q K^T;  P = exp2(c S - m);  O = P V
+//
+// A work unit has up to 128 query rows, the M of one tcgen05.mma; unused rows cost
+// nothing but the products. Per tile of 64 tokens: S (128 x 64, fp32) accumulates in TMEM,
+// twice, so that the next tile's scores are formed while this one's softmax runs; a thread
+// owns a row (no shuffles); P goes to shared memory as bf16 and O (128 x d, fp32) stays in
+// TMEM. O is rescaled only when a row's maximum has grown by more than 2^8 since the last
+// time (P and the sums stay within range until then, and the quotient is the same).
+// Warps: four of softmax, one issues the products, one loads tiles by TMA.
+//
+// Bound: a tile of 64 tokens at d = 256 is 64 KB of HBM, about 2700 cycles of an SM's share;
+// its products take about 1000 and the softmax of 128 rows about 1500.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <mutex>
+
+#include "gdn_attn.h"
+#include "gdn_attn_device.cuh"
+#include "gdn_tcgen05.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kTile = 64, kRowTile = 128, kThreads = 256, kSoftmaxWarps = 4;
+#ifndef GDN_ROWS_COST
+#define GDN_ROWS_COST 4
+#endif
+#ifndef GDN_ROWS_MIN_SHARE
+#define GDN_ROWS_MIN_SHARE 8
+#endif
+constexpr int kCost = GDN_ROWS_COST;           // places of a unit beside its tiles'
+constexpr int kMinShare = GDN_ROWS_MIN_SHARE;  // places of a CTA at least
+constexpr float kRescale = 8.0f;               // growth of a row's maximum (log2) that makes it the new reference
+
+template <int D>
+struct RowsGeo {
+    static constexpr int NB = D / 64;               // 128-byte blocks of a token's key
+    static constexpr int TILEB = kTile * D * 2;     // bytes of a tile of keys (values)
+    static constexpr int SLOTS = D == 256 ? 2 : (D == 128 ? 5 : 8);  // tiles of keys, and of values, in flight
+    static constexpr int QB = kRowTile * D * 2, PB = kRowTile * kTile * 2;
+    static constexpr int O_COL = 128;               // TMEM columns: S at 0 and 64, O from here
+    static constexpr int FIXED = 1024;
+    static constexpr size_t SMEM = QB + PB + 2 * SLOTS * TILEB + FIXED;
+};
+
+// Instruction descriptor of kind::f16: D fp32, A and B bf16, A K-major, B K-major or
+// MN-major, M = 128, N = n.
+constexpr uint32_t idesc_of(int n, int b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(kRowTile >> 4) << 24);
+}
+// Shared-memory descriptor of a tile in 8-row by 128-byte atoms with the 128-byte swizzle.
+// K-major: `stride` from one 8-row group to the next. MN-major: `lead` from one 64-element
+// block to the next, `stride` from one group of 8 along K to the next.
+__device__ __forceinline__ uint64_t atoms_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUtensorMap map_k,
+                 const __grid_constant__ CUtensorMap map_v, const int box) {
+    using Gm = RowsGeo<D>;
+    constexpr int NB = Gm::NB, TILEB = Gm::TILEB, SLOTS = Gm::SLOTS, CPR = D / 8;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    unsigned char* kring = smem;
+    unsigned char* vring = kring + SLOTS * TILEB;
+    unsigned char* qbuf = vring + SLOTS * TILEB;   // [NB blocks][128 rows][128 bytes], swizzled
+    unsigned char* pbuf = qbuf + Gm::QB;           // [128 rows][128 bytes], swizzled
+    Piece* pieces = reinterpret_cast<Piece*>(pbuf + Gm::PB);          // [2] by turns, then the share's first and last split ones
+    uint64_t* kfull = reinterpret_cast<uint64_t*>(pieces + 4);        // [SLOTS] each
+    uint64_t* kempty = kfull + SLOTS;
+    uint64_t* vfull = kempty + SLOTS;
+    uint64_t* vempty = vfull + SLOTS;
+    uint64_t* sfull = vempty + SLOTS;   // [2] scores formed
+    uint64_t* sfree = sfull + 2;        // [2] scores read
+    uint64_t* pready = sfree + 2;       // probabilities written (and O rescaled)
+    uint64_t* pvdone = pready + 1;      // O complete up to a tile
+    uint64_t* qfull = pvdone + 1;       // a unit's queries and description are there
+    uint64_t* qfree = qfull + 1;        // its scores are all formed
+    uint64_t* sbar = qfree + 1;         // the softmax warps' own barrier
+    uint64_t* cbar = sbar + 1;          // all warps'
+    int* misc = reinterpret_cast<int*>(cbar + 1);  // [16] sums; 8, 9: tile skipped by the products; 10: TMEM; 12: last to arrive; 15: stop
+    int* prefix = misc + 16;                       // [B + 1]
+    volatile int* stop = misc + 15;
+    volatile int* skip = misc + 8;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int Hkv = p.sh.Hkv, G = p.sh.G;
+
+    if (tid == 0) {
+        for (int i = 0; i < SLOTS; ++i) {
+            mbar_init(kfull + i, 1);
+            mbar_init(kempty + i, 1);
+            mbar_init(vfull + i, 1);
+            mbar_init(vempty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(sfull + i, 1);
+            mbar_init(sfree + i, kSoftmaxWarps);
+            skip[i] = 0;
+        }
+        mbar_init(pready, kSoftmaxWarps);
+        mbar_init(pvdone, 1);
+        mbar_init(qfull, kSoftmaxWarps);
+        mbar_init(qfree, 1);
+        mbar_init(sbar, kSoftmaxWarps);
+        mbar_init(cbar, kThreads / 32);
+        *stop = 0;
+        mbar_init_fence();
+        fence_proxy_async_smem();
+    }
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+
+    Share<kRowTile, kTile, 0, kCost, kCost> at(p, prefix);
+    at.template sum_batch<kThreads>(prefix, misc);
+    if (!at.begin(kMinShare)) return;
+    if (warp == 4) tmem_alloc(smem_addr(misc + 10), 512);
+    tcgen05_fence_before();
+    __syncthreads();
+    tcgen05_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc + 10);
+
+    auto give_up = [&] { return *stop != 0; };
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (mbar_wait_deadline(bar, parity, kWaitTimeoutCycles, give_up)) return true;
+        if (*stop == 0) attn_abort(p.err_flag, stop);
+        return false;
+    };
+    bool split_first = false, split_last = false;
+    // the share's pieces in order: every role walks them by itself; false after the last
+    auto next_piece = [&](Piece& u) {
+        const Seq c = at.s;
+        const int rt = at.unit / Hkv, place = at.place, from = at.tile;
+        u = Piece{c.n, c.first, c.past, c.lo, c.base, at.unit - rt * Hkv, rt, from, min(c.tiles - from, at.hi - place - from), 0,
+                  at.cta_of(place), at.cta_of(place + c.tiles - 1)};
+        if (u.c0 != u.c1) {
+            const int which = (int)blockIdx.x == u.c0;
+            if (which) split_last = true; else split_first = true;
+            if (tid == 0) pieces[2 + which] = u;
+        }
+        u.last = !at.next_unit();
+        at.tile = 0;
+    };
+
+    if (warp == 5) {
+        // ================= loading: tile n's keys and values =================
+        const int x = lane * box < kTile ? lane : -1;  // this lane's part of a tile
+        int n = 0, issued[2] = {0, 0};
+        bool more = true;
+        while (more) {
+            const int st = n % SLOTS, turn = n / SLOTS, h = at.unit % Hkv;
+            const int tok = x >= 0 ? at.look_up(at.s.base + at.tile * kTile + x * box, box) : -1;
+            const unsigned bytes = __popc(__ballot_sync(0xffffffffu, tok >= 0)) * box * D * 2;
+            bool ok = true;
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                uint64_t* full = (v ? vfull : kfull) + st;
+                if (turn > 0 && !(ok = wait((v ? vempty : kempty) + st, (turn - 1) & 1))) break;
+                if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+                __syncwarp();
+                if (tok >= 0) tma_load_5d(smem_addr((v ? vring : kring) + st * TILEB) + x * box * D * 2, v ? &map_v : &map_k, tok >> 3, h, smem_addr(full));
+                ++issued[v];
+            }
+            if (!ok) break;
+            ++n;
+            more = at.advance(1);
+        }
+        // what is still in flight lands before the block leaves (all of it has, unless a wait ran out)
+        for (int v = 0; v < 2; ++v) {
+            for (int i = max(0, issued[v] - SLOTS); i < issued[v]; ++i) mbar_wait_bounded((v ? vfull : kfull) + i % SLOTS, (i / SLOTS) & 1);
+        }
+    } else if (warp == 4) {
+        // ================= products: one thread =================
+        if (lane == 0) {
+            constexpr uint32_t qk = idesc_of(kTile, 0), pv = idesc_of(D, 1);
+            const uint32_t q0 = smem_addr(qbuf), p0 = smem_addr(pbuf);
+            bool ok = true, started = false;
+            auto accumulate = [&](int n) {  // O += P V of tile n
+                const int st = n % SLOTS;
+                if (!wait(pready, n & 1) || !wait(vfull + st, (n / SLOTS) & 1)) return false;
+                tcgen05_fence_after();
+                if (!skip[n & 1]) {
+                    const uint32_t v = smem_addr(vring + st * TILEB);
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        umma_bf16(tmem + Gm::O_COL, atoms_desc(p0 + k * 32, 16, 1024), atoms_desc(v + k * 2 * NB * 1024, 1024, NB * 1024), pv,
+                                  started || k > 0);
+                }
+                skip[n & 1] = 0;
+                started = true;
+                umma_commit(smem_addr(vempty + st));
+                umma_commit(smem_addr(pvdone));
+                return true;
+            };
+            int n = 0;
+            Piece u;
+            u.last = 0;
+            for (int ord = 0; ok && !u.last; ++ord) {
+                next_piece(u);
+                if (!(ok = wait(qfull, ord & 1))) break;
+                started = false;
+                for (int i = 0; i < u.count; ++i, ++n) {
+                    const int st = n % SLOTS;
+                    if (!(ok = wait(kfull + st, (n / SLOTS) & 1) && (n < 2 || wait(sfree + (n & 1), ((n >> 1) - 1) & 1)))) break;
+                    tcgen05_fence_after();
+                    const uint32_t k = smem_addr(kring + st * TILEB);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        umma_bf16(tmem + (n & 1) * kTile, atoms_desc(q0 + (kk / 4) * (kRowTile * 128) + (kk % 4) * 32, 16, 1024),
+                                  atoms_desc(k + (kk / 4) * 1024 + (kk % 4) * 32, 16, NB * 1024), qk, kk > 0);
+                    umma_commit(smem_addr(kempty + st));
+                    umma_commit(smem_addr(sfull + (n & 1)));
+                    if (i == u.count - 1) umma_commit(smem_addr(qfree));
+                    if (i > 0 && !(ok = accumulate(n - 1))) break;
+                }
+                if (ok) ok = accumulate(n - 1);
+            }
+        }
+        __syncwarp();
+    } else if (warp < kSoftmaxWarps) {
+        // ================= softmax: thread = row =================
+        const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+        const bool capped = p.sh.softcap > 0.0f;
+        const float to_log2 = capped ? p.sh.softcap * kLog2e : p.sh.sm_scale * kLog2e;
+        const float factor = capped ? 2.0f * kLog2e * p.sh.sm_scale / p.sh.softcap : to_log2;
+        const int inv_g = 65536 / G + 1;
+        unsigned char* prow = pbuf + tid * 128;
+        uint32_t sphase = 0;
+        auto arrive = [&](uint64_t* bar) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        bool ok = true;
+        int n = 0;
+        Piece u;
+        u.last = 0;
+        for (int ord = 0; ok && !u.last; ++ord) {
+            next_piece(u);
+            const int rows = min(kRowTile, u.n * G - u.rt * kRowTile), kv_len = u.past + u.n;
+            const int rr = u.rt * kRowTile + tid, t = (rr * inv_g) >> 16, head = u.h * G + rr - t * G;
+            // the unit's queries, a warp a row at a time (rows past the last: zeros)
+            if (ord > 0 && !(ok = wait(qfree, (ord - 1) & 1))) break;
+#pragma unroll 4
+            for (int r = warp; r < kRowTile; r += kSoftmaxWarps) {
+                const int qr = u.rt * kRowTile + r, qt = (qr * inv_g) >> 16;
+                const uint16_t* src = p.q.ptr;
+                if (r < rows) src += (size_t)(u.first + qt) * p.q.row + (size_t)(u.h * G + qr - qt * G) * p.q.head;
+                for (int c = lane; c < CPR; c += 32)
+                    cp16(smem_addr(qbuf + (c >> 3) * (kRowTile * 128) + r * 128 + (((c ^ r) & 7) << 4)), r < rows ? src + c * 8 : p.q.ptr, r < rows);
+            }
+            cp_wait_all();
+            fence_proxy_async_smem();
+            arrive(qfull);
+            if (p.gate.ptr && tid < rows) {  // the gates' lines into L2: they are read when the unit ends
+                const uint16_t* line = p.gate.ptr + (size_t)(u.first + t) * p.gate.row + (size_t)head * p.gate.head;
+#pragma unroll
+                for (int i = 0; i < NB; ++i) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(line + i * 64));
+            }
+            const bool active = warp * 32 < rows;
+            // this row attends positions lo .. hi-1; every row of the unit those from all_lo to all_hi
+            const int hi = min(u.past + t + 1, kv_len), lo = p.sh.window > 0 ? u.past + t + 1 - p.sh.window : 0;
+            const int all_lo = p.sh.window > 0 ? max(0, kv_len - p.sh.window) : 0, all_hi = u.past + 1;
+            float ref = -INFINITY, sum = 0.0f;  // the row's reference (log2 units) and sum
+            for (int i = 0; i < u.count; ++i, ++n) {
+                const int pos0 = u.base + (u.tile + i) * kTile;
+                const bool whole = pos0 >= all_lo && pos0 + kTile <= all_hi;
+                if (!(ok = wait(sfull + (n & 1), (n >> 1) & 1))) break;
+                tcgen05_fence_after();
+                float x[kTile];
+                if (active) {
+                    tmem_ld32(lanes + (n & 1) * kTile, *reinterpret_cast<float(*)[32]>(x));
+                    tmem_ld32(lanes + (n & 1) * kTile + 32, *reinterpret_cast<float(*)[32]>(x + 32));
+                }
+                tcgen05_fence_before();
+                arrive(sfree + (n & 1));
+                float top = -INFINITY;
+                if (active) {
+                    if (capped) {
+#pragma unroll
+                        for (int c = 0; c < kTile; ++c)  // c tanh(y) = c - 2 c / (1 + e^2y)
+                            x[c] = fmaf(-2.0f * to_log2, rcp_fast(1.0f + exp2_fast(x[c] * factor)), to_log2);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < kTile; ++c) x[c] *= factor;
+                    }
+                    if (!whole) {
+#pragma unroll
+                        for (int c = 0; c < kTile; ++c) x[c] = pos0 + c < hi && pos0 + c >= lo ? x[c] : -INFINITY;
+                    }
+#pragma unroll
+                    for (int c = 0; c < kTile; ++c) top = fmaxf(top, x[c]);
+                }
+                // the tile before is in O, and its probabilities are read
+                if (i > 0 && !(ok = wait(pvdone, (n - 1) & 1))) break;
+                if (active) {
+                    const bool grow = i == 0 || top > ref + kRescale || ref == -INFINITY;
+                    const float next = grow ? fmaxf(top, ref) : ref;
+                    if (i > 0 && __any_sync(0xffffffffu, next != ref)) {
+                        const float f = next == -INFINITY ? 1.0f : exp2_fast(ref - next);
+                        sum *= f;
+                        tcgen05_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            float o[32];
+                            uint32_t z[32];
+                            tmem_ld32(lanes + Gm::O_COL + c, o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) z[e] = __float_as_uint(o[e] * f);
+                            tmem_st32(lanes + Gm::O_COL + c, z);
+                        }
+                        tmem_wait_st();
+                    }
+                    ref = next;
+                    const float from = ref == -INFINITY ? 0.0f : ref;  // nothing seen yet
+#pragma unroll
+                    for (int c = 0; c < kTile; c += 8) {
+                        uint32_t z[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float a = exp2_fast(x[c + 2 * e] - from), b = exp2_fast(x[c + 2 * e + 1] - from);
+                            sum += a + b;
+                            z[e] = pack2<false>(a, b);
+                        }
+                        *reinterpret_cast<uint4*>(prow + ((((c >> 3) ^ tid) & 7) << 4)) = make_uint4(z[0], z[1], z[2], z[3]);
+                    }
+                }
+                if (!whole) {
+                    // Values outside the sequence become zeros. A value that is not finite must not reach
+                    // the rows whose mask leaves it out (0 * inf): such a tile skips the products and goes
+                    // token by token.
+                    if (!(ok = wait(vfull + n % SLOTS, (n / SLOTS) & 1))) break;
+                    unsigned char* vt = vring + (n % SLOTS) * TILEB;
+                    bool bad = false;
+                    for (int k = lane; k < 16 * CPR; k += 32) {
+                        const int r = warp * 16 + k / CPR;
+                        uint4* word = reinterpret_cast<uint4*>(vt + chunk_at<CPR>(r, k % CPR));
+                        if (pos0 + r < u.lo || pos0 + r >= kv_len) {
+                            *word = make_uint4(0, 0, 0, 0);
+                            continue;
+                        }
+                        const uint4 w = *word;
+                        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) bad |= (v[e] & 0x7f80u) == 0x7f80u || (v[e] & 0x7f800000u) == 0x7f800000u;
+                    }
+                    if (__any_sync(0xffffffffu, bad) && lane == 0) skip[n & 1] = 1;
+                    arrive(sbar);
+                    if (!(ok = wait(sbar, sphase))) break;
+                    sphase ^= 1;
+                    if (skip[n & 1] && active) {
+                        tcgen05_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            float o[32];
+                            uint32_t z[32];
+                            if (i > 0) tmem_ld32(lanes + Gm::O_COL + c, o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = i > 0 ? o[e] : 0.0f;
+#pragma unroll 1
+                            for (int k = 0; k < kTile; ++k) {
+                                if (pos0 + k >= hi || pos0 + k < lo) continue;
+                                const float f = bf16_bits_to_float(*reinterpret_cast<const uint16_t*>(prow + ((((k >> 3) ^ tid) & 7) << 4) + (k & 7) * 2));
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    o[e] = fmaf(f, bf16_bits_to_float(*reinterpret_cast<const uint16_t*>(vt + chunk_at<CPR>(k, (c + e) >> 3) + (e & 7) * 2)), o[e]);
+                            }
+                            __syncwarp();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) z[e] = __float_as_uint(o[e]);
+                            tmem_st32(lanes + Gm::O_COL + c, z);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                tcgen05_fence_before();
+                fence_proxy_async_smem();
+                arrive(pready);
+            }
+            if (!ok || !(ok = wait(pvdone, (n - 1) & 1))) break;
+            tcgen05_fence_after();
+            if (active) {
+                float* mine = p.partial + (size_t)(blockIdx.x * 2 + ((int)blockIdx.x == u.c0)) * (kRowTile * (D + 2));
+                const bool split = u.c0 != u.c1;
+                const size_t row = (size_t)u.first + t;
+                const float inv = 1.0f / sum;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    tmem_ld32(lanes + Gm::O_COL + c, o);
+                    if (tid >= rows) continue;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 v = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        if (split) *reinterpret_cast<float4*>(mine + tid * D + c + e) = v;
+                        else write_out4(p, row, head, D, c + e, v, inv);
+                    }
+                }
+                if (tid < rows) {
+                    if (split) {
+                        mine[kRowTile * D + tid] = ref;
+                        mine[kRowTile * D + kRowTile + tid] = sum;
+                    } else if (p.lse) {
+                        p.lse[row * p.sh.Hq + head] = (ref + log2f(sum)) * kLn2;
+                    }
+                }
+            }
+            tcgen05_fence_before();  // O is read before the next unit's products overwrite it (they wait for its queries)
+        }
+    } else {
+        Piece u;
+        u.last = 0;
+        while (!u.last) next_piece(u);
+    }
+    // all roles are done (or have given up): the tensor memory goes back
+    __syncthreads();
+    if (warp == 4) {
+        tcgen05_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (*stop != 0) return;
+    if (warp == 4 || warp == 5) {  // they have walked the share in other steps
+        split_first = false;
+        split_last = false;
+    }
+    uint32_t cphase = 0;
+    auto meet = [&]() -> bool {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(cbar);
+        const bool done = wait(cbar, cphase);
+        cphase ^= 1;
+        return done;
+    };
+    // whether pieces are split is the same for all: from thread 0
+    if (tid == 0) {
+        misc[0] = split_first;
+        misc[1] = split_last;
+    }
+    __syncthreads();
+    static_assert(kRowTile * (kAttnMaxCtas + 2) * 4 <= 2 * SLOTS * TILEB, "weights");
+    join_units<D, kRowTile, kThreads>(p, pieces + 2, misc[0] != 0, misc[1] != 0, reinterpret_cast<float*>(smem), misc + 12, meet);
+}
+
+template <int D>
+cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
+    using Gm = RowsGeo<D>;
+    auto kern = attn_rows_kernel<D>;
+    static_assert(4 * sizeof(Piece) + (4 * Gm::SLOTS + 10) * 8 + 16 * 4 <= Gm::FIXED, "small data");
+    static_assert(Gm::SMEM + (kAttnMaxBatch + 1) * 4 <= 227 * 1024, "shared memory");
+    int dev, sms;
+    cudaError_t e = device_sms(&dev, &sms);
+    if (e != cudaSuccess) return e;
+    static std::once_flag once[kMaxDevices];
+    static cudaError_t set[kMaxDevices];
+    std::call_once(once[dev], [&] {
+        set[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    });
+    if (set[dev] != cudaSuccess) return set[dev];
+    int box = a.sh.page_size & -a.sh.page_size;
+    if (box > kTile) box = kTile;
+    CUtensorMap map_k{}, map_v{};
+    if (!make_pool_map(&map_k, a.c.k, a, D * 2, box) || !make_pool_map(&map_v, a.c.v, a, D * 2, box)) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(sms < kAttnMaxCtas ? sms : kAttnMaxCtas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Gm::SMEM + ((size_t)a.B + 1) * 4;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, map_k, map_v, box);
+}
+
+}  // namespace
+
+// Rows per key/value head from which this kernel is the faster one (see the comment at the
+// launch of the other).
+bool attn_rows_supported(bool fp8, int page_size, int rows) { return !fp8 && page_size % 8 == 0 && rows > kAttnFewRows; }
+
+cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t stream) {
+    switch (a.sh.d) {
+        case 64: return launch<64>(a, stream);
+        case 128: return launch<128>(a, stream);
+        case 256: return launch<256>(a, stream);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace gdn
