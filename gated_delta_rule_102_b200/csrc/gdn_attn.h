@@ -71,9 +71,6 @@ constexpr int kAttnMaxBatch = 2048;
 #define GDN_ATTN_FEW 16
 #endif
 constexpr int kAttnFewRows = GDN_ATTN_FEW;  // query rows per key/value head that the kernel for few rows takes in any case
-// query rows and tokens of a work unit's tiles for `rows` rows per key/value head
-int attn_row_tile(int d, bool fp8, int page_size, int rows);
-int attn_token_tile(int d, bool fp8, int page_size, int rows);
 size_t attn_workspace_bytes(int d, bool fp8, int page_size, int rows);
 
 cudaError_t launch_qk_rope_append(const AppendArgs& a, cudaStream_t stream);

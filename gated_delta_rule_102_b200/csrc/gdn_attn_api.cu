@@ -175,10 +175,9 @@ gdn_status gdn_attn_decode(const gdn_attn_config* cfg, const gdn_kv_cache* cache
     if (misaligned(out, 16) || misaligned(lse, 4) || misaligned(slots, 4) || misaligned(err_flag, 4) ||
         misaligned(workspace, 16))
         return GDN_ERR_MISALIGNED;
-    // the kernel numbers its work units (token tiles of a row tile of a head) in 32 bits
-    const int rows = T * a.sh.G, tt = gdn::attn_token_tile(a.sh.d, a.sh.fp8, a.sh.page_size, rows),
-              rt = gdn::attn_row_tile(a.sh.d, a.sh.fp8, a.sh.page_size, rows);
-    const double tiles = (double)B * (ceil((double)a.c.max_pages * a.sh.page_size / tt) + 8) * a.sh.Hkv * ((rows + rt - 1) / rt);
+    // the kernels number the batch's work (token tiles of a row tile of a head) in 32 bits
+    const int rows = T * a.sh.G;
+    const double tiles = (double)B * (ceil((double)a.c.max_pages * a.sh.page_size / 16) + 16) * a.sh.Hkv * ((rows + 15) / 16);
     if (tiles > 2.0e9) return GDN_ERR_UNSUPPORTED;
     a.B = B;
     a.T = T;
@@ -190,8 +189,11 @@ gdn_status gdn_attn_decode(const gdn_attn_config* cfg, const gdn_kv_cache* cache
     a.err_flag = err_flag;
     a.counters = static_cast<unsigned int*>(workspace);
     a.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + gdn::kAttnCounters * sizeof(unsigned int));
-    return from_cuda(gdn::attn_rows_supported(a.sh.fp8, a.sh.page_size, rows) ? gdn::launch_attn_rows(a, (cudaStream_t)stream)
-                                                                              : gdn::launch_attn_decode(a, (cudaStream_t)stream));
+    // (a broadcast row or head, stride 0, has no tensor map: the kernel for few rows takes it, whose
+    // partial results are smaller)
+    const bool broadcast = (a.q.row == 0 && total_tokens > 1) || (a.q.head == 0 && a.sh.Hq > 1);
+    const bool many = gdn::attn_rows_supported(a.sh.fp8, a.sh.page_size, rows) && !broadcast;
+    return from_cuda(many ? gdn::launch_attn_rows(a, (cudaStream_t)stream) : gdn::launch_attn_decode(a, (cudaStream_t)stream));
 }
 
 size_t gdn_attn_decode_workspace_bytes(const gdn_attn_config* cfg, int32_t B, int32_t T) {

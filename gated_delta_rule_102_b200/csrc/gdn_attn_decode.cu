@@ -132,7 +132,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
-    Share<BM, ST, kSingle, kShortCost, kUnitCost> at(p, prefix);
+    Share<ST, kSingle, kShortCost, kUnitCost> at(p, BM, prefix);
     at.template sum_batch<kAttnThreads>(prefix, misc);
     if (!at.begin(kMinShare)) return;
 
@@ -164,6 +164,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
     if (warp == kComputeWarps + kLoadWarps) {
         // ================= queries =================
         bool more_units = true;
+        int sent = 0;
         for (int ord = 0; more_units; ++ord) {
             const Seq c = at.s;
             const int rt = at.unit / Hkv, h = at.unit - rt * Hkv, place = at.place, from = at.tile;
@@ -173,7 +174,8 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
             // are left as they are (a row's products touch no other row)
             const int qs = ord % NQ, rows = min(BM, c.n * G - rt * BM);
             const int inv_g = 65536 / G + 1;  // r / G = r * inv_g >> 16 for r < 320, G <= 16
-            if (!wait_count(qfreed + qs, ord / NQ * kComputeWarps)) return;
+            if (!wait_count(qfreed + qs, ord / NQ * kComputeWarps)) break;
+            sent = ord + 1;
             unsigned char* q = qbuf + qs * QB;
             if (lane == 0) {
                 pieces[qs] = Piece{c.n, c.first, c.past, c.lo, c.base, h, rt, from, min(c.tiles - from, at.hi - place - from),
@@ -228,6 +230,10 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                 }
             }
         }
+        // after an abort: what is in flight lands before the block leaves
+        if (*stop != 0 && !FP8) {
+            for (int i = max(0, sent - NQ); i < sent; ++i) mbar_wait_bounded(qfull + i % NQ, (i / NQ) & 1);
+        }
         return;
     }
 
@@ -253,10 +259,12 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
         const int chunk = lane % CPR, sub = lane / CPR;
         bool more_slots = pw == 0 || at.advance(pw);
         if (more_slots) find_tokens();
+        int sent = -1;
         for (int i = pw; more_slots; i += kLoadWarps) {
             const int h = at.unit % Hkv, st = i % SLOTS, turn = i / SLOTS;
             if (!wait_count(freed + st, turn * Gm::READERS)) break;
             const uint32_t dst = smem_addr(ring + st * Gm::SLOTB);
+            sent = i;
             if (box) {
                 const unsigned got = __ballot_sync(0xffffffffu, tok[0] >= 0);
                 if (lane == 0) mbar_arrive_expect_tx(full + st, __popc(got) * box * Gm::ROWB);
@@ -292,6 +300,9 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
             if (more_slots) find_tokens();
         }
         cp_wait_all();
+        if (*stop != 0 && box) {  // as above
+            for (int i = sent; i >= 0 && i > sent - SLOTS; i -= kLoadWarps) mbar_wait_bounded(full + i % SLOTS, (i / SLOTS) & 1);
+        }
         return;
     }
 
@@ -705,8 +716,8 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
         }
     }
 
-    static_assert(BM * (kAttnMaxCtas + 2) * 4 <= SLOTS * Gm::SLOTB, "weights");
-    join_units<D, BM, kComputeWarps * 32>(p, pieces + NQ, split_first, split_last, reinterpret_cast<float*>(ring), misc + 12, meet);
+    static_assert(BM * (kJoinMost + 2) * 4 <= SLOTS * Gm::SLOTB, "weights");
+    join_units<D, BM, kComputeWarps * 32>(p, pieces + NQ, split_first, split_last, BM, reinterpret_cast<float*>(ring), misc + 12, meet);
 }
 
 template <int D, bool FP8, int WM>
@@ -752,21 +763,6 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
 // Row groups for `rows` query rows per key/value head.
 int row_groups(int rows) { return rows <= 16 ? 1 : (rows <= 32 ? 2 : 4); }
 
-// Calls f(integral_constant-like geometry) for the kernel that a shape selects.
-template <typename F>
-auto with_geometry(int d, bool fp8, int rows, F f) {
-    const int wm = row_groups(rows);
-#define GDN_PICK(D)                                                                     \
-    if (fp8) return wm == 1 ? f(Geo<D, true, 1>{}) : wm == 2 ? f(Geo<D, true, 2>{}) : f(Geo<D, true, 4>{}); \
-    return wm == 1 ? f(Geo<D, false, 1>{}) : wm == 2 ? f(Geo<D, false, 2>{}) : f(Geo<D, false, 4>{});
-    switch (d) {
-        case 64: GDN_PICK(64)
-        case 128: GDN_PICK(128)
-        default: GDN_PICK(256)
-    }
-#undef GDN_PICK
-}
-
 template <int D, bool FP8>
 cudaError_t launch_rows(const AttnArgs& a, cudaStream_t stream) {
     switch (row_groups(a.T * a.sh.G)) {
@@ -778,17 +774,9 @@ cudaError_t launch_rows(const AttnArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-int attn_row_tile(int d, bool fp8, int page_size, int rows) {
-    if (attn_rows_supported(fp8, page_size, rows)) return 128;
-    return with_geometry(d, fp8, rows, [](auto g) { return decltype(g)::BM; });
-}
-int attn_token_tile(int d, bool fp8, int page_size, int rows) {
-    if (attn_rows_supported(fp8, page_size, rows)) return 64;
-    return with_geometry(d, fp8, rows, [](auto g) { return decltype(g)::ST; });
-}
 size_t attn_workspace_bytes(int d, bool fp8, int page_size, int rows) {
-    return kAttnCounters * sizeof(unsigned int) +
-           (size_t)kAttnMaxCtas * 2 * attn_row_tile(d, fp8, page_size, rows) * (d + 2) * sizeof(float);
+    const int tile = attn_rows_supported(fp8, page_size, rows) ? 128 : 16 * row_groups(rows);
+    return kAttnCounters * sizeof(unsigned int) + (size_t)kAttnMaxCtas * 2 * tile * (d + 2) * sizeof(float);
 }
 
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t stream) {

@@ -17,6 +17,8 @@ namespace gdn {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kJoinFlat = 12, kJoinGroup = 8;  // pieces of a unit that one CTA joins at once, and groups of more
+constexpr int kJoinMost = (kAttnMaxCtas + kJoinGroup - 1) / kJoinGroup;
+static_assert(kJoinMost >= kJoinFlat, "pieces joined at once");
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
     const int n = valid ? 16 : 0;  // 0: the 16 bytes are filled with zeros and nothing is read
@@ -118,8 +120,8 @@ static __device__ __noinline__ void attn_abort(int32_t* err_flag, volatile int* 
 
 // ---------------------------------------------------------------------------------
 // The schedule. The G query heads of a key/value head and a sequence's n new tokens form
-// n * G query rows that read the same keys, so a work unit is (sequence, row tile of BM
-// rows, key/value head) and costs its number of tiles of ST tokens, plus some for its
+// n * G query rows that read the same keys, so a work unit is (sequence, row tile,
+// key/value head) and costs its number of tiles of ST tokens, plus some for its
 // beginning and end. All units' costs in a row are "places"; the CTAs get equal,
 // contiguous shares of them. It follows from the lengths alone, which are read on the
 // device: every CTA sums the batch.
@@ -141,16 +143,17 @@ struct Piece {
     int c0, c1;                    // the CTAs that share the unit
 };
 
-// BM rows and ST tokens a tile; a unit of at most SHORT tiles costs SHORT_COST more, any other COST.
-template <int BM, int ST, int SHORT, int SHORT_COST, int COST>
+// Tiles of ST tokens; a unit of at most SHORT tiles costs SHORT_COST more, any other COST.
+template <int ST, int SHORT, int SHORT_COST, int COST>
 struct Share {
     const AttnArgs& p;
+    const int row_tile;  // query rows of a unit
     const int* prefix;  // [B + 1] (shared memory) places before each sequence
     int Hkv, total, ctas, per, more, lo, hi;
     Seq s;
     int b, unit, place, tile;  // where we are: unit = row_tile * Hkv + head, the place of its first tile, the tile
 
-    __device__ __forceinline__ Share(const AttnArgs& args, const int* prefix_) : p(args), prefix(prefix_), Hkv(args.sh.Hkv) {}
+    __device__ __forceinline__ Share(const AttnArgs& args, int row_tile_, const int* prefix_) : p(args), row_tile(row_tile_), prefix(prefix_), Hkv(args.sh.Hkv) {}
 
     __device__ __forceinline__ Seq load(int i, bool report) const {
         Seq q;
@@ -186,7 +189,7 @@ struct Share {
         q.base = q.lo & ~(ST - 1);
         q.tiles = (q.past + q.n - q.base + ST - 1) / ST;
         q.cost = q.tiles <= SHORT ? SHORT_COST : COST;
-        q.row_tiles = (q.n * p.sh.G + BM - 1) / BM;
+        q.row_tiles = (q.n * p.sh.G + row_tile - 1) / row_tile;
         return q;
     }
 
@@ -313,20 +316,20 @@ __device__ __forceinline__ void write_out4(const AttnArgs& p, size_t row, int he
 // groups of kJoinGroup first (by the last CTA of the group, into its first piece's place),
 // then the groups: at 74 pieces of 8 KB one CTA alone would read 600 KB.
 // All NT threads that meet() joins, after each has written its part of the pieces.
-// shared_pieces: the share's first and last split piece; wt: BM * (kAttnMaxCtas + 2) floats and
-// flag: one int of shared memory.
+// shared_pieces: the share's first and last split piece; wt: BM * (kJoinMost + 2) floats and
+// flag: one int of shared memory. row_tile: query rows of a unit (BM, or fewer).
 template <int D, int BM, int NT, typename Meet>
 __device__ __forceinline__ bool join_units(const AttnArgs& p, const Piece* shared_pieces, bool split_first, bool split_last,
-                                           float* wt, volatile int* flag, Meet meet) {
-    constexpr int WP = kAttnMaxCtas + 2, PSTRIDE = BM * (D + 2);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = p.sh.G;
+                                           int row_tile, float* wt, volatile int* flag, Meet meet) {
+    constexpr int WP = kJoinMost + 2, PSTRIDE = BM * (D + 2);
+    const int tid = threadIdx.x, G = p.sh.G, inv_g = 65536 / G + 1;  // r / G = r * inv_g >> 16 for r < 320, G <= 16
     if (!split_first && !split_last) return true;
     __threadfence();
     if (!meet()) return false;
     for (int which = 0; which < 2; ++which) {
         if (!(which ? split_last : split_first)) continue;
         const Piece u = shared_pieces[which];
-        const int rows = min(BM, u.n * G - u.rt * BM), all = u.c1 - u.c0 + 1;
+        const int rows = min(row_tile, u.n * G - u.rt * row_tile), all = u.c1 - u.c0 + 1;
         auto place_of = [&](int i) { return p.partial + (size_t)((u.c0 + i) * 2 + (i == 0)) * PSTRIDE; };
         const bool flat = all <= kJoinFlat;
         for (int level = flat ? 1 : 0; level < 2; ++level) {
@@ -339,65 +342,82 @@ __device__ __forceinline__ bool join_units(const AttnArgs& p, const Piece* share
             if (!meet()) return false;
             if (!*flag) break;  // (written next after another meeting)
             __threadfence();
-            auto part = [&](int i) -> const float* { return place_of(from + i * step); };
-            for (int r = warp; r < rows; r += NT / 32) {
-                float* w = wt + r * WP;
+            const float* first = place_of(from);
+            const float* rest = place_of(from + step);  // of the second piece, the others at equal distances
+            const size_t stride = (size_t)step * 2 * PSTRIDE;
+            auto part = [&](int i) { return i == 0 ? first : rest + (size_t)(i - 1) * stride; };
+            // (never more than kAttnMaxCtas / kJoinGroup pieces here: a thread a row)
+            if (tid < rows) {
+                float* w = wt + tid * WP;
                 float top = -INFINITY, tot = 0.0f;
-                for (int i = lane; i < count; i += 32) {
-                    w[i] = __ldcg(part(i) + BM * D + r);
+#pragma unroll 8
+                for (int i = 0; i < count; ++i) {
+                    w[i] = __ldcg(part(i) + BM * D + tid);
                     top = fmaxf(top, w[i]);
                 }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                for (int i = lane; i < count; i += 32) {
-                    w[i] = w[i] == -INFINITY ? 0.0f : exp2_fast(w[i] - top);
-                    tot = fmaf(w[i], __ldcg(part(i) + BM * D + BM + r), tot);
+#pragma unroll 8
+                for (int i = 0; i < count; ++i) {
+                    const float f = w[i] == -INFINITY ? 0.0f : exp2_fast(w[i] - top);
+                    tot = fmaf(f, __ldcg(part(i) + BM * D + BM + tid), tot);
+                    w[i] = f;
                 }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-                if (lane == 0) {
-                    w[kAttnMaxCtas] = tot;
-                    w[kAttnMaxCtas + 1] = top;
-                }
+                w[kJoinMost] = tot;
+                w[kJoinMost + 1] = top;
             }
             if (!meet()) return false;
-            for (int k = tid; k < rows * (D / 4); k += NT) {
-                const int r = k / (D / 4), col = (k % (D / 4)) * 4;
-                const float* w = wt + r * WP;
-                const float* src = part(0) + r * D + col;
-                const float* rest = count > 1 ? part(1) + r * D + col : src;
-                const size_t stride = (size_t)step * 2 * PSTRIDE;
-                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                for (int i0 = 0; i0 < count; i0 += 10) {
-                    float4 x[10];
+            // four columns by kItems rows a thread, so that their loads are in flight together
+            constexpr int kItems = BM > 16 ? 4 : 2;
+            const int items = rows * (D / 4);
+            for (int k0 = tid; k0 < items; k0 += kItems * NT) {
+                float4 o[kItems];
 #pragma unroll
-                    for (int i = 0; i < 10; ++i) {
-                        const float* at = i0 + i == 0 ? src : rest + (size_t)(i0 + i - 1) * stride;
-                        x[i] = i0 + i < count ? __ldcg(reinterpret_cast<const float4*>(at)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int y = 0; y < kItems; ++y) o[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int i0 = 0; i0 < count; i0 += 4) {
+                    float4 x[4][kItems];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float* at = part(i0 + i);
+#pragma unroll
+                        for (int y = 0; y < kItems; ++y) {
+                            const int k = k0 + y * NT;
+                            x[i][y] = i0 + i < count && k < items ? __ldcg(reinterpret_cast<const float4*>(at) + k)
+                                                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        }
                     }
 #pragma unroll
-                    for (int i = 0; i < 10; ++i) {
-                        const float f = i0 + i < count ? w[i0 + i] : 0.0f;
-                        o.x = fmaf(f, x[i].x, o.x);
-                        o.y = fmaf(f, x[i].y, o.y);
-                        o.z = fmaf(f, x[i].z, o.z);
-                        o.w = fmaf(f, x[i].w, o.w);
+                    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                        for (int y = 0; y < kItems; ++y) {
+                            const int k = k0 + y * NT;
+                            const float f = i0 + i < count && k < items ? wt[k / (D / 4) * WP + i0 + i] : 0.0f;
+                            o[y].x = fmaf(f, x[i][y].x, o[y].x);
+                            o[y].y = fmaf(f, x[i][y].y, o[y].y);
+                            o[y].z = fmaf(f, x[i][y].z, o[y].z);
+                            o[y].w = fmaf(f, x[i][y].w, o[y].w);
+                        }
                     }
                 }
-                if (level == 0) {
-                    *reinterpret_cast<float4*>(place_of(from) + r * D + col) = o;
-                    continue;
+#pragma unroll
+                for (int y = 0; y < kItems; ++y) {
+                    const int k = k0 + y * NT;
+                    if (k >= items) break;
+                    if (level == 0) {
+                        reinterpret_cast<float4*>(place_of(from))[k] = o[y];
+                        continue;
+                    }
+                    const int r = k / (D / 4), col = (k % (D / 4)) * 4;
+                    const int rr = u.rt * row_tile + r, t = (rr * inv_g) >> 16, head = u.h * G + rr - t * G;
+                    const size_t row = (size_t)u.first + t;
+                    const float* w = wt + r * WP;
+                    write_out4(p, row, head, D, col, o[y], p.sh.v_scale / w[kJoinMost]);
+                    if (p.lse && col == 0) p.lse[row * p.sh.Hq + head] = (w[kJoinMost + 1] + log2f(w[kJoinMost])) * kLn2;
                 }
-                const int rr = u.rt * BM + r, t = rr / G, head = u.h * G + rr - t * G;
-                const size_t row = (size_t)u.first + t;
-                write_out4(p, row, head, D, col, o, p.sh.v_scale / w[kAttnMaxCtas]);
-                if (p.lse && col == 0) p.lse[row * p.sh.Hq + head] = (w[kAttnMaxCtas + 1] + log2f(w[kAttnMaxCtas])) * kLn2;
             }
             if (tid == 0) *counter = 0;
             if (level == 0 && tid < rows) {  // the group's maximum and sum, in place of its first piece's
                 float* to = place_of(from) + BM * D;
-                to[tid] = wt[tid * WP + kAttnMaxCtas + 1];
-                to[BM + tid] = wt[tid * WP + kAttnMaxCtas];
+                to[tid] = wt[tid * WP + kJoinMost + 1];
+                to[BM + tid] = wt[tid * WP + kJoinMost];
             }
             if (level == 0) __threadfence();
             if (!meet()) return false;  // the next weights go where these are

@@ -66,7 +66,8 @@ __device__ __forceinline__ uint64_t atoms_desc(uint32_t addr, uint32_t lead, uin
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUtensorMap map_k,
-                 const __grid_constant__ CUtensorMap map_v, const int box) {
+                 const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_q, const int box,
+                 const int q_tokens) {
     using Gm = RowsGeo<D>;
     constexpr int NB = Gm::NB, TILEB = Gm::TILEB, SLOTS = Gm::SLOTS, CPR = D / 8;
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -83,7 +84,7 @@ attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUt
     uint64_t* sfree = sfull + 2;        // [2] scores read
     uint64_t* pready = sfree + 2;       // probabilities written (and O rescaled)
     uint64_t* pvdone = pready + 1;      // O complete up to a tile
-    uint64_t* qfull = pvdone + 1;       // a unit's queries and description are there
+    uint64_t* qfull = pvdone + 1;       // a unit's queries are there
     uint64_t* qfree = qfull + 1;        // its scores are all formed
     uint64_t* sbar = qfree + 1;         // the softmax warps' own barrier
     uint64_t* cbar = sbar + 1;          // all warps'
@@ -108,7 +109,7 @@ attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUt
         }
         mbar_init(pready, kSoftmaxWarps);
         mbar_init(pvdone, 1);
-        mbar_init(qfull, kSoftmaxWarps);
+        mbar_init(qfull, 1);
         mbar_init(qfree, 1);
         mbar_init(sbar, kSoftmaxWarps);
         mbar_init(cbar, kThreads / 32);
@@ -119,7 +120,9 @@ attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUt
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
-    Share<kRowTile, kTile, 0, kCost, kCost> at(p, prefix);
+    // a unit's rows are whole tokens, so that a TMA box brings them
+    const int row_tile = kRowTile / G * G, inv_g = 65536 / G + 1;  // r / G = r * inv_g >> 16 for r < 320, G <= 16
+    Share<kTile, 0, kCost, kCost> at(p, row_tile, prefix);
     at.template sum_batch<kThreads>(prefix, misc);
     if (!at.begin(kMinShare)) return;
     if (warp == 4) tmem_alloc(smem_addr(misc + 10), 512);
@@ -231,7 +234,6 @@ attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUt
         const bool capped = p.sh.softcap > 0.0f;
         const float to_log2 = capped ? p.sh.softcap * kLog2e : p.sh.sm_scale * kLog2e;
         const float factor = capped ? 2.0f * kLog2e * p.sh.sm_scale / p.sh.softcap : to_log2;
-        const int inv_g = 65536 / G + 1;
         unsigned char* prow = pbuf + tid * 128;
         uint32_t sphase = 0;
         auto arrive = [&](uint64_t* bar) {
@@ -244,21 +246,8 @@ attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUt
         u.last = 0;
         for (int ord = 0; ok && !u.last; ++ord) {
             next_piece(u);
-            const int rows = min(kRowTile, u.n * G - u.rt * kRowTile), kv_len = u.past + u.n;
-            const int rr = u.rt * kRowTile + tid, t = (rr * inv_g) >> 16, head = u.h * G + rr - t * G;
-            // the unit's queries, a warp a row at a time (rows past the last: zeros)
-            if (ord > 0 && !(ok = wait(qfree, (ord - 1) & 1))) break;
-#pragma unroll 4
-            for (int r = warp; r < kRowTile; r += kSoftmaxWarps) {
-                const int qr = u.rt * kRowTile + r, qt = (qr * inv_g) >> 16;
-                const uint16_t* src = p.q.ptr;
-                if (r < rows) src += (size_t)(u.first + qt) * p.q.row + (size_t)(u.h * G + qr - qt * G) * p.q.head;
-                for (int c = lane; c < CPR; c += 32)
-                    cp16(smem_addr(qbuf + (c >> 3) * (kRowTile * 128) + r * 128 + (((c ^ r) & 7) << 4)), r < rows ? src + c * 8 : p.q.ptr, r < rows);
-            }
-            cp_wait_all();
-            fence_proxy_async_smem();
-            arrive(qfull);
+            const int rows = min(row_tile, u.n * G - u.rt * row_tile), kv_len = u.past + u.n;
+            const int rr = u.rt * row_tile + tid, t = (rr * inv_g) >> 16, head = u.h * G + rr - t * G;
             if (p.gate.ptr && tid < rows) {  // the gates' lines into L2: they are read when the unit ends
                 const uint16_t* line = p.gate.ptr + (size_t)(u.first + t) * p.gate.row + (size_t)head * p.gate.head;
 #pragma unroll
@@ -391,16 +380,29 @@ attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUt
                 const bool split = u.c0 != u.c1;
                 const size_t row = (size_t)u.first + t;
                 const float inv = 1.0f / sum;
+                // a row's 32 columns through this warp's part of the probabilities' memory, so that
+                // eight lanes write a row together
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     float o[32];
                     tmem_ld32(lanes + Gm::O_COL + c, o);
-                    if (tid >= rows) continue;
+                    __syncwarp();
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 v = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                        if (split) *reinterpret_cast<float4*>(mine + tid * D + c + e) = v;
-                        else write_out4(p, row, head, D, c + e, v, inv);
+                    for (int e = 0; e < 8; ++e)
+                        *reinterpret_cast<float4*>(prow + (((e ^ tid) & 7) << 4)) = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = warp * 32 + e * 4 + (lane >> 3), q = lane & 7;
+                        const float4 v = *reinterpret_cast<const float4*>(pbuf + r * 128 + (((q ^ r) & 7) << 4));
+                        const float scale = __shfl_sync(0xffffffffu, inv, e * 4 + (lane >> 3));
+                        if (r >= rows) continue;
+                        if (split) {
+                            *reinterpret_cast<float4*>(mine + r * D + c + q * 4) = v;
+                        } else {
+                            const int qr = u.rt * row_tile + r, qt = (qr * inv_g) >> 16;
+                            write_out4(p, (size_t)u.first + qt, u.h * G + qr - qt * G, D, c + q * 4, v, scale);
+                        }
                     }
                 }
                 if (tid < rows) {
@@ -414,6 +416,30 @@ attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUt
             }
             tcgen05_fence_before();  // O is read before the next unit's products overwrite it (they wait for its queries)
         }
+    } else if (warp == 6) {
+        // ================= queries =================
+        Piece u;
+        u.last = 0;
+        int ord = 0;
+        for (; !u.last; ++ord) {
+            next_piece(u);
+            if (ord > 0 && !wait(qfree, (ord - 1) & 1)) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(qfull, NB * G * q_tokens * 128);
+                // q_tokens tokens of G heads, a 128-byte block at a time; what lies past the sequence's
+                // tokens is other rows (or zeros), whose products touch no row of this unit
+                for (int k = 0; k < NB; ++k) {
+                    asm volatile(
+                        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+                        "%3, %4, %5}], [%6];\n" ::"r"(smem_addr(qbuf + k * (kRowTile * 128))),
+                        "l"(reinterpret_cast<uint64_t>(&map_q)), "r"(0), "r"(u.h * G), "r"(u.first + u.rt * (kRowTile / G)), "r"(k),
+                        "r"(smem_addr(qfull))
+                        : "memory");
+                }
+            }
+            __syncwarp();
+        }
+        if (ord > 0) mbar_wait_bounded(qfull, (ord - 1) & 1);  // as for the tiles
     } else {
         Piece u;
         u.last = 0;
@@ -444,8 +470,8 @@ attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUt
         misc[1] = split_last;
     }
     __syncthreads();
-    static_assert(kRowTile * (kAttnMaxCtas + 2) * 4 <= 2 * SLOTS * TILEB, "weights");
-    join_units<D, kRowTile, kThreads>(p, pieces + 2, misc[0] != 0, misc[1] != 0, reinterpret_cast<float*>(smem), misc + 12, meet);
+    static_assert(kRowTile * (kJoinMost + 2) * 4 <= 2 * SLOTS * TILEB, "weights");
+    join_units<D, kRowTile, kThreads>(p, pieces + 2, misc[0] != 0, misc[1] != 0, row_tile, reinterpret_cast<float*>(smem), misc + 12, meet);
 }
 
 template <int D>
@@ -467,6 +493,16 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
     if (box > kTile) box = kTile;
     CUtensorMap map_k{}, map_v{};
     if (!make_pool_map(&map_k, a.c.k, a, D * 2, box) || !make_pool_map(&map_v, a.c.v, a, D * 2, box)) return cudaErrorInvalidValue;
+    // queries as [128-byte block][token][head][byte], in boxes of a unit's tokens by G heads
+    const int q_tokens = a.T < kRowTile / a.sh.G ? a.T : kRowTile / a.sh.G;
+    CUtensorMap map_q{};
+    {
+        // (a single row or head may come with a stride of 0, which no map takes and nothing uses)
+        const cuuint64_t dims[4] = {64, (cuuint64_t)a.sh.Hq, (cuuint64_t)a.total, (cuuint64_t)Gm::NB};
+        const cuuint64_t strides[3] = {(cuuint64_t)(a.q.head ? a.q.head * 2 : 16), (cuuint64_t)(a.q.row ? a.q.row * 2 : 16), 128};
+        const cuuint32_t boxes[4] = {64, (cuuint32_t)a.sh.G, (cuuint32_t)q_tokens, 1};
+        if (!encode_tensor_map(&map_q, false, 4, const_cast<uint16_t*>(a.q.ptr), dims, strides, boxes, 128)) return cudaErrorInvalidValue;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(sms < kAttnMaxCtas ? sms : kAttnMaxCtas));
     cfg.blockDim = dim3(kThreads);
@@ -477,7 +513,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, a, map_k, map_v, box);
+    return cudaLaunchKernelEx(&cfg, kern, a, map_k, map_v, map_q, box, q_tokens);
 }
 
 }  // namespace
