@@ -49,6 +49,15 @@ struct AppendArgs {
     int32_t* err_flag;
 };
 
+// A CTA's piece of a unit, as its loading warps describe it to the computing ones.
+struct Piece {
+    int n, first, past, lo, base;  // of the sequence
+    int h, rt;                     // key/value head, row tile
+    int tile, count;               // its first tile and how many
+    int last;                      // the share ends with it
+    int c0, c1;                    // the CTAs that share the unit
+};
+
 struct AttnArgs {
     AttnShape sh;
     PagedCache c;
@@ -60,12 +69,14 @@ struct AttnArgs {
     float* lse;
     int32_t* err_flag;
     unsigned int* counters;  // workspace: kAttnCounters zeroed counters, left zeroed
+    Piece* split;            // workspace: kAttnMaxCtas units that go on in the next CTA (many rows)
     float* partial;          // workspace: two partial results per CTA
 };
 
 // CTAs of the attention kernel (one per SM, at most this many) and the workspace.
 constexpr int kAttnMaxCtas = 192;
 constexpr int kAttnCounters = 3 * kAttnMaxCtas;  // arrivals at units, and at groups of their pieces
+constexpr size_t kAttnPartialAt = kAttnCounters * sizeof(unsigned int) + kAttnMaxCtas * sizeof(Piece);  // workspace offset
 constexpr int kAttnMaxBatch = 2048;
 #ifndef GDN_ATTN_FEW
 #define GDN_ATTN_FEW 16

@@ -188,7 +188,9 @@ gdn_status gdn_attn_decode(const gdn_attn_config* cfg, const gdn_kv_cache* cache
     a.lse = lse;
     a.err_flag = err_flag;
     a.counters = static_cast<unsigned int*>(workspace);
-    a.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + gdn::kAttnCounters * sizeof(unsigned int));
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    a.split = reinterpret_cast<gdn::Piece*>(ws + gdn::kAttnCounters * sizeof(unsigned int));
+    a.partial = reinterpret_cast<float*>(ws + gdn::kAttnPartialAt);
     // (a broadcast row or head, stride 0, has no tensor map: the kernel for few rows takes it, whose
     // partial results are smaller)
     const bool broadcast = (a.q.row == 0 && total_tokens > 1) || (a.q.head == 0 && a.sh.Hq > 1);

@@ -126,6 +126,10 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
         }
         mbar_init(cbar, kComputeWarps);
         *stop = 0;
+        if (box) {
+            asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&map_k)) : "memory");
+            asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&map_v)) : "memory");
+        }
         mbar_init_fence();
         fence_proxy_async_smem();
     }
@@ -776,7 +780,7 @@ cudaError_t launch_rows(const AttnArgs& a, cudaStream_t stream) {
 
 size_t attn_workspace_bytes(int d, bool fp8, int page_size, int rows) {
     const int tile = attn_rows_supported(fp8, page_size, rows) ? 128 : 16 * row_groups(rows);
-    return kAttnCounters * sizeof(unsigned int) + (size_t)kAttnMaxCtas * 2 * tile * (d + 2) * sizeof(float);
+    return kAttnPartialAt + (size_t)kAttnMaxCtas * 2 * tile * (d + 2) * sizeof(float);
 }
 
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t stream) {

@@ -134,15 +134,6 @@ struct Seq {
     int row_tiles;
 };
 
-// A CTA's piece of a unit, as its loading warps describe it to the computing ones.
-struct Piece {
-    int n, first, past, lo, base;  // of the sequence
-    int h, rt;                     // key/value head, row tile
-    int tile, count;               // its first tile and how many
-    int last;                      // the share ends with it
-    int c0, c1;                    // the CTAs that share the unit
-};
-
 // Tiles of ST tokens; a unit of at most SHORT tiles costs SHORT_COST more, any other COST.
 template <int ST, int SHORT, int SHORT_COST, int COST>
 struct Share {
@@ -292,14 +283,17 @@ struct Share {
     }
 };
 
-// Four columns of an output row: normalised, gated, rounded once.
-__device__ __forceinline__ void write_out4(const AttnArgs& p, size_t row, int head, int d, int col, float4 o, float inv) {
+// Four columns of an output row: their gates (read apart, so that many are in flight), and the
+// values normalised, gated and rounded once.
+__device__ __forceinline__ uint2 gate_of4(const AttnArgs& p, size_t row, int head, int col) {
+    return __ldg(reinterpret_cast<const uint2*>(p.gate.ptr + row * p.gate.row + (size_t)head * p.gate.head + col));
+}
+__device__ __forceinline__ void write_out4(const AttnArgs& p, size_t row, int head, int d, int col, float4 o, float inv, uint2 z) {
     o.x *= inv;
     o.y *= inv;
     o.z *= inv;
     o.w *= inv;
     if (p.gate.ptr) {
-        const uint2 z = __ldg(reinterpret_cast<const uint2*>(p.gate.ptr + row * p.gate.row + (size_t)head * p.gate.head + col));
         o.x *= sigmoid_fast(__uint_as_float(z.x << 16));
         o.y *= sigmoid_fast(__uint_as_float(z.x & 0xffff0000u));
         o.z *= sigmoid_fast(__uint_as_float(z.y << 16));
@@ -366,16 +360,22 @@ __device__ __forceinline__ bool join_units(const AttnArgs& p, const Piece* share
             }
             if (!meet()) return false;
             // four columns by kItems rows a thread, so that their loads are in flight together
-            constexpr int kItems = BM > 16 ? 4 : 2;
+            constexpr int kItems = BM == 128 ? 8 : (BM > 16 ? 4 : 2), kPieces = BM == 128 ? 3 : 4;
             const int items = rows * (D / 4);
             for (int k0 = tid; k0 < items; k0 += kItems * NT) {
                 float4 o[kItems];
+                uint2 z[kItems];
 #pragma unroll
-                for (int y = 0; y < kItems; ++y) o[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                for (int i0 = 0; i0 < count; i0 += 4) {
-                    float4 x[4][kItems];
+                for (int y = 0; y < kItems; ++y) {
+                    const int k = k0 + y * NT, r = k / (D / 4), rr = u.rt * row_tile + r, t = (rr * inv_g) >> 16;
+                    o[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    z[y] = make_uint2(0, 0);
+                    if (p.gate.ptr && level == 1 && k < items) z[y] = gate_of4(p, (size_t)u.first + t, u.h * G + rr - t * G, (k % (D / 4)) * 4);
+                }
+                for (int i0 = 0; i0 < count; i0 += kPieces) {
+                    float4 x[kPieces][kItems];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < kPieces; ++i) {
                         const float* at = part(i0 + i);
 #pragma unroll
                         for (int y = 0; y < kItems; ++y) {
@@ -385,7 +385,7 @@ __device__ __forceinline__ bool join_units(const AttnArgs& p, const Piece* share
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < kPieces; ++i) {
 #pragma unroll
                         for (int y = 0; y < kItems; ++y) {
                             const int k = k0 + y * NT;
@@ -400,7 +400,7 @@ __device__ __forceinline__ bool join_units(const AttnArgs& p, const Piece* share
 #pragma unroll
                 for (int y = 0; y < kItems; ++y) {
                     const int k = k0 + y * NT;
-                    if (k >= items) break;
+                    if (k >= items) continue;
                     if (level == 0) {
                         reinterpret_cast<float4*>(place_of(from))[k] = o[y];
                         continue;
@@ -409,7 +409,7 @@ __device__ __forceinline__ bool join_units(const AttnArgs& p, const Piece* share
                     const int rr = u.rt * row_tile + r, t = (rr * inv_g) >> 16, head = u.h * G + rr - t * G;
                     const size_t row = (size_t)u.first + t;
                     const float* w = wt + r * WP;
-                    write_out4(p, row, head, D, col, o[y], p.sh.v_scale / w[kJoinMost]);
+                    write_out4(p, row, head, D, col, o[y], p.sh.v_scale / w[kJoinMost], z[y]);
                     if (p.lse && col == 0) p.lse[row * p.sh.Hq + head] = (w[kJoinMost + 1] + log2f(w[kJoinMost])) * kLn2;
                 }
             }

@@ -75,8 +75,7 @@ attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUt
     unsigned char* vring = kring + SLOTS * TILEB;
     unsigned char* qbuf = vring + SLOTS * TILEB;   // [NB blocks][128 rows][128 bytes], swizzled
     unsigned char* pbuf = qbuf + Gm::QB;           // [128 rows][128 bytes], swizzled
-    Piece* pieces = reinterpret_cast<Piece*>(pbuf + Gm::PB);          // [2] by turns, then the share's first and last split ones
-    uint64_t* kfull = reinterpret_cast<uint64_t*>(pieces + 4);        // [SLOTS] each
+    uint64_t* kfull = reinterpret_cast<uint64_t*>(pbuf + Gm::PB);  // [SLOTS] each
     uint64_t* kempty = kfull + SLOTS;
     uint64_t* vfull = kempty + SLOTS;
     uint64_t* vempty = vfull + SLOTS;
@@ -87,8 +86,7 @@ attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUt
     uint64_t* qfull = pvdone + 1;       // a unit's queries are there
     uint64_t* qfree = qfull + 1;        // its scores are all formed
     uint64_t* sbar = qfree + 1;         // the softmax warps' own barrier
-    uint64_t* cbar = sbar + 1;          // all warps'
-    int* misc = reinterpret_cast<int*>(cbar + 1);  // [16] sums; 8, 9: tile skipped by the products; 10: TMEM; 12: last to arrive; 15: stop
+    int* misc = reinterpret_cast<int*>(sbar + 1);  // [16] sums; 8, 9: tile skipped by the products; 10: TMEM; 15: stop
     int* prefix = misc + 16;                       // [B + 1]
     volatile int* stop = misc + 15;
     volatile int* skip = misc + 8;
@@ -112,7 +110,6 @@ attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUt
         mbar_init(qfull, 1);
         mbar_init(qfree, 1);
         mbar_init(sbar, kSoftmaxWarps);
-        mbar_init(cbar, kThreads / 32);
         *stop = 0;
         mbar_init_fence();
         fence_proxy_async_smem();
@@ -124,7 +121,14 @@ attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUt
     const int row_tile = kRowTile / G * G, inv_g = 65536 / G + 1;  // r / G = r * inv_g >> 16 for r < 320, G <= 16
     Share<kTile, 0, kCost, kCost> at(p, row_tile, prefix);
     at.template sum_batch<kThreads>(prefix, misc);
-    if (!at.begin(kMinShare)) return;
+    const bool any = at.begin(kMinShare);
+    if (tid == 0) p.split[blockIdx.x].count = 0;  // no unit to join from here on, unless one is found
+    if (!any) return;
+    if (tid == 0) {
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&map_k)) : "memory");
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&map_v)) : "memory");
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&map_q)) : "memory");
+    }
     if (warp == 4) tmem_alloc(smem_addr(misc + 10), 512);
     tcgen05_fence_before();
     __syncthreads();
@@ -137,18 +141,14 @@ attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUt
         if (*stop == 0) attn_abort(p.err_flag, stop);
         return false;
     };
-    bool split_first = false, split_last = false;
-    // the share's pieces in order: every role walks them by itself; false after the last
+    // the share's pieces in order: every role walks them by itself
     auto next_piece = [&](Piece& u) {
         const Seq c = at.s;
         const int rt = at.unit / Hkv, place = at.place, from = at.tile;
         u = Piece{c.n, c.first, c.past, c.lo, c.base, at.unit - rt * Hkv, rt, from, min(c.tiles - from, at.hi - place - from), 0,
                   at.cta_of(place), at.cta_of(place + c.tiles - 1)};
-        if (u.c0 != u.c1) {
-            const int which = (int)blockIdx.x == u.c0;
-            if (which) split_last = true; else split_first = true;
-            if (tid == 0) pieces[2 + which] = u;
-        }
+        // the CTA with the first piece of a unit that goes on tells the launch that joins them
+        if (u.c0 != u.c1 && (int)blockIdx.x == u.c0 && tid == 0) p.split[blockIdx.x] = u;
         u.last = !at.next_unit();
         at.tile = 0;
     };
@@ -384,6 +384,13 @@ attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUt
                 // eight lanes write a row together
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
+                    uint2 z[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = warp * 32 + e * 4 + (lane >> 3), qr = u.rt * row_tile + r, qt = (qr * inv_g) >> 16;
+                        z[e] = make_uint2(0, 0);
+                        if (!split && p.gate.ptr && r < rows) z[e] = gate_of4(p, (size_t)u.first + qt, u.h * G + qr - qt * G, c + (lane & 7) * 4);
+                    }
                     float o[32];
                     tmem_ld32(lanes + Gm::O_COL + c, o);
                     __syncwarp();
@@ -401,7 +408,7 @@ attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUt
                             *reinterpret_cast<float4*>(mine + r * D + c + q * 4) = v;
                         } else {
                             const int qr = u.rt * row_tile + r, qt = (qr * inv_g) >> 16;
-                            write_out4(p, (size_t)u.first + qt, u.h * G + qr - qt * G, D, c + q * 4, v, scale);
+                            write_out4(p, (size_t)u.first + qt, u.h * G + qr - qt * G, D, c + q * 4, v, scale, z[e]);
                         }
                     }
                 }
@@ -440,10 +447,6 @@ attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUt
             __syncwarp();
         }
         if (ord > 0) mbar_wait_bounded(qfull, (ord - 1) & 1);  // as for the tiles
-    } else {
-        Piece u;
-        u.last = 0;
-        while (!u.last) next_piece(u);
     }
     // all roles are done (or have given up): the tensor memory goes back
     __syncthreads();
@@ -451,34 +454,101 @@ attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUt
         tcgen05_fence_after();
         tmem_dealloc(tmem, 512);
     }
-    if (*stop != 0) return;
-    if (warp == 4 || warp == 5) {  // they have walked the share in other steps
-        split_first = false;
-        split_last = false;
+}
+
+// ---------------------------------------------------------------------------------
+// The units that several CTAs share, joined by a launch of its own: a partial result is
+// 128 KB here (128 rows of 256), and the last CTA of a unit alone took 25 us for its
+// pieces while the others had nothing left to do; spread over all SMs, 16 rows of a unit
+// a block, it is a few. Block (c, y): rows 16 y on of the unit whose first piece ends the
+// share of CTA c.
+constexpr int kJoinRows = 16;
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) attn_rows_join_kernel(const __grid_constant__ AttnArgs p) {
+    constexpr int PSTRIDE = kRowTile * (D + 2), WP = kAttnMaxCtas + 2;
+    constexpr int ITEMS = kJoinRows * (D / 4) / kThreads;  // float4s of a thread
+    __shared__ float wt[kJoinRows * WP];  // weights of a row's pieces, then their sum and maximum
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = p.sh.G;
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    const Piece u = p.split[blockIdx.x];
+    if (u.count == 0) return;
+    const int row_tile = kRowTile / G * G, rows = min(row_tile, u.n * G - u.rt * row_tile), base = blockIdx.y * kJoinRows;
+    if (base >= rows) return;
+    const int pieces = u.c1 - u.c0 + 1, inv_g = 65536 / G + 1;
+    const float* first = p.partial + (size_t)(u.c0 * 2 + 1) * PSTRIDE;
+    const float* rest = p.partial + (size_t)(u.c0 + 1) * 2 * PSTRIDE;
+    auto part = [&](int i) { return i == 0 ? first : rest + (size_t)(i - 1) * (2 * PSTRIDE); };
+    for (int r = warp; r < kJoinRows; r += kThreads / 32) {
+        float* w = wt + r * WP;
+        float top = -INFINITY, tot = 0.0f;
+        for (int i = lane; i < pieces; i += 32) {
+            w[i] = __ldcg(part(i) + kRowTile * D + base + r);
+            top = fmaxf(top, w[i]);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int i = lane; i < pieces; i += 32) {
+            w[i] = w[i] == -INFINITY ? 0.0f : exp2_fast(w[i] - top);
+            tot = fmaf(w[i], __ldcg(part(i) + kRowTile * D + kRowTile + base + r), tot);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+        if (lane == 0) {
+            w[kAttnMaxCtas] = tot;
+            w[kAttnMaxCtas + 1] = top;
+        }
     }
-    uint32_t cphase = 0;
-    auto meet = [&]() -> bool {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(cbar);
-        const bool done = wait(cbar, cphase);
-        cphase ^= 1;
-        return done;
-    };
-    // whether pieces are split is the same for all: from thread 0
-    if (tid == 0) {
-        misc[0] = split_first;
-        misc[1] = split_last;
+    float4 o[ITEMS];
+    uint2 z[ITEMS];
+#pragma unroll
+    for (int y = 0; y < ITEMS; ++y) {
+        const int k = tid + y * kThreads, rr = u.rt * row_tile + base + k / (D / 4), t = (rr * inv_g) >> 16;
+        o[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        z[y] = make_uint2(0, 0);
+        if (p.gate.ptr && base + k / (D / 4) < rows) z[y] = gate_of4(p, (size_t)u.first + t, u.h * G + rr - t * G, k % (D / 4) * 4);
     }
     __syncthreads();
-    static_assert(kRowTile * (kJoinMost + 2) * 4 <= 2 * SLOTS * TILEB, "weights");
-    join_units<D, kRowTile, kThreads>(p, pieces + 2, misc[0] != 0, misc[1] != 0, row_tile, reinterpret_cast<float*>(smem), misc + 12, meet);
+    for (int i0 = 0; i0 < pieces; i0 += 4) {
+        float4 x[4][ITEMS];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4* at = reinterpret_cast<const float4*>(part(min(i0 + i, pieces - 1)) + base * D);
+#pragma unroll
+            for (int y = 0; y < ITEMS; ++y) x[i][y] = __ldcg(at + tid + y * kThreads);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i0 + i >= pieces) break;
+#pragma unroll
+            for (int y = 0; y < ITEMS; ++y) {
+                const float f = wt[(tid + y * kThreads) / (D / 4) * WP + i0 + i];
+                if (f == 0.0f) continue;  // (a piece without a token for the row says nothing, whatever it holds)
+                o[y].x = fmaf(f, x[i][y].x, o[y].x);
+                o[y].y = fmaf(f, x[i][y].y, o[y].y);
+                o[y].z = fmaf(f, x[i][y].z, o[y].z);
+                o[y].w = fmaf(f, x[i][y].w, o[y].w);
+            }
+        }
+    }
+#pragma unroll
+    for (int y = 0; y < ITEMS; ++y) {
+        const int k = tid + y * kThreads, r = k / (D / 4), col = k % (D / 4) * 4;
+        if (base + r >= rows) continue;
+        const int rr = u.rt * row_tile + base + r, t = (rr * inv_g) >> 16, head = u.h * G + rr - t * G;
+        const size_t row = (size_t)u.first + t;
+        const float* w = wt + r * WP;
+        write_out4(p, row, head, D, col, o[y], 1.0f / w[kAttnMaxCtas], z[y]);
+        if (p.lse && col == 0) p.lse[row * p.sh.Hq + head] = (w[kAttnMaxCtas + 1] + log2f(w[kAttnMaxCtas])) * kLn2;
+    }
 }
 
 template <int D>
 cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
     using Gm = RowsGeo<D>;
     auto kern = attn_rows_kernel<D>;
-    static_assert(4 * sizeof(Piece) + (4 * Gm::SLOTS + 10) * 8 + 16 * 4 <= Gm::FIXED, "small data");
+    static_assert((4 * Gm::SLOTS + 9) * 8 + 16 * 4 <= Gm::FIXED, "small data");
     static_assert(Gm::SMEM + (kAttnMaxBatch + 1) * 4 <= 227 * 1024, "shared memory");
     int dev, sms;
     cudaError_t e = device_sms(&dev, &sms);
@@ -513,7 +583,10 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, a, map_k, map_v, map_q, box, q_tokens);
+    if ((e = cudaLaunchKernelEx(&cfg, kern, a, map_k, map_v, map_q, box, q_tokens)) != cudaSuccess) return e;
+    cfg.gridDim.y = (unsigned)(((a.T * a.sh.G < kRowTile ? a.T * a.sh.G : kRowTile) + kJoinRows - 1) / kJoinRows);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, attn_rows_join_kernel<D>, a);
 }
 
 }  // namespace
