@@ -151,7 +151,21 @@ __global__ void __launch_bounds__(kT) pages_reserve_kernel(const PageArgs p) {
 // copy_dst of a pair that was skipped (-1: forked, nothing to copy)
 constexpr int kSkipped = -2;
 
-__global__ void __launch_bounds__(kT) pages_fork_kernel(const PageArgs p) {
+// The whole pages of a forked child: the parent's, with one holder more. Threads begin, begin + step, ..
+__device__ __forceinline__ void share_pages(const PageArgs& p, int i, int begin, int step) {
+    if (p.copy_dst[i] == kSkipped) return;
+    const int src = p.src_slots[i], full = p.seq_lens[src] / p.page_size;
+    const int32_t* parent = p.table + (long)src * p.max_pages;
+    int32_t* child = p.table + (long)p.slots[i] * p.max_pages;
+    for (int j = begin; j < full; j += step) {
+        const int e = parent[j];
+        child[j] = e;
+        if (e >= 0 && e < p.num_pages) atomicAdd(p.refs + e, 1);
+        else flag(p.err_flag, GDN_DEVICE_ERR_PAGE_BIT);
+    }
+}
+
+__global__ void __launch_bounds__(kT) pages_fork_kernel(const PageArgs p, const bool share) {
     __shared__ int warp_sums[kWarps], prefix[kPagesMaxBatch + 1];
     pdl_wait();
     const int ps = p.page_size;
@@ -204,22 +218,14 @@ __global__ void __launch_bounds__(kT) pages_fork_kernel(const PageArgs p) {
         if (p.copy_dst[i] != kSkipped) p.seq_lens[p.slots[i]] = p.seq_lens[p.src_slots[i]];
         else p.copy_src[i] = -1;
     }
+    if (!share) return;
+    __syncthreads();
+    for (int i = threadIdx.x >> 5; i < p.n; i += kWarps) share_pages(p, i, threadIdx.x & 31, 32);
 }
 
-// The whole pages of every forked child: the parent's, with one holder more.
 __global__ void __launch_bounds__(256) pages_share_kernel(const PageArgs p) {
     pdl_wait();
-    const int i = blockIdx.x;
-    if (p.copy_dst[i] == kSkipped) return;
-    const int src = p.src_slots[i], full = p.seq_lens[src] / p.page_size;
-    const int32_t* parent = p.table + (long)src * p.max_pages;
-    int32_t* child = p.table + (long)p.slots[i] * p.max_pages;
-    for (int j = blockIdx.y * 256 + threadIdx.x; j < full; j += gridDim.y * 256) {
-        const int e = parent[j];
-        child[j] = e;
-        if (e >= 0 && e < p.num_pages) atomicAdd(p.refs + e, 1);
-        else flag(p.err_flag, GDN_DEVICE_ERR_PAGE_BIT);
-    }
+    share_pages(p, blockIdx.x, blockIdx.y * 256 + threadIdx.x, gridDim.y * 256);
 }
 
 __global__ void __launch_bounds__(256) pages_free_kernel(const PageArgs p) {
@@ -363,8 +369,8 @@ __global__ void __launch_bounds__(256, 4) copy_rows_kernel(const __grid_constant
     }
 }
 
-template <typename K, typename A>
-cudaError_t launch(K kernel, dim3 grid, int threads, const A& a, cudaStream_t stream) {
+template <typename K, typename... A>
+cudaError_t launch(K kernel, dim3 grid, int threads, cudaStream_t stream, const A&... a) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
@@ -374,7 +380,7 @@ cudaError_t launch(K kernel, dim3 grid, int threads, const A& a, cudaStream_t st
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    return cudaLaunchKernelEx(&cfg, kernel, a...);
 }
 
 // CTAs that share one table row of up to max_pages entries (four entries a thread).
@@ -386,26 +392,28 @@ int row_ctas(int max_pages) {
 }  // namespace
 
 cudaError_t launch_pages_reserve(const PageArgs& a, cudaStream_t stream) {
-    return launch(pages_reserve_kernel, dim3(1), kT, a, stream);
+    return launch(pages_reserve_kernel, dim3(1), kT, stream, a);
 }
 
 cudaError_t launch_pages_fork(const PageArgs& a, cudaStream_t stream) {
-    const cudaError_t e = launch(pages_fork_kernel, dim3(1), kT, a, stream);
-    if (e != cudaSuccess) return e;
-    return launch(pages_share_kernel, dim3(a.n, row_ctas(a.max_pages)), 256, a, stream);
+    // a few thousand table entries are shared by the CTA that allocates; more pay for a launch of their own
+    const bool share = (long)a.n * a.max_pages <= 4096;
+    const cudaError_t e = launch(pages_fork_kernel, dim3(1), kT, stream, a, share);
+    if (e != cudaSuccess || share) return e;
+    return launch(pages_share_kernel, dim3(a.n, row_ctas(a.max_pages)), 256, stream, a);
 }
 
 cudaError_t launch_pages_free(const PageArgs& a, cudaStream_t stream) {
-    return launch(pages_free_kernel, dim3(a.n, row_ctas(a.max_pages)), 256, a, stream);
+    return launch(pages_free_kernel, dim3(a.n, row_ctas(a.max_pages)), 256, stream, a);
 }
 
 cudaError_t launch_pages_compact(const PageArgs& a, cudaStream_t stream) {
     int dev, sms;
     cudaError_t e = device_sms(&dev, &sms);
     if (e != cudaSuccess) return e;
-    if ((e = launch(pages_compact_kernel, dim3(1), kT, a, stream)) != cudaSuccess) return e;
+    if ((e = launch(pages_compact_kernel, dim3(1), kT, stream, a)) != cudaSuccess) return e;
     const long n = ((long)a.rows * a.max_pages + 1023) / 1024;
-    return launch(pages_renumber_kernel, dim3((unsigned)(n < sms * 8 ? n : sms * 8)), 256, a, stream);
+    return launch(pages_renumber_kernel, dim3((unsigned)(n < sms * 8 ? n : sms * 8)), 256, stream, a);
 }
 
 cudaError_t launch_copy_rows(CopyArgs& a, cudaStream_t stream) {
@@ -419,7 +427,7 @@ cudaError_t launch_copy_rows(CopyArgs& a, cudaStream_t stream) {
     }
     a.first_chunk[a.n_bufs] = chunks;
     const long ctas = (chunks * a.n_max + 7) / 8;
-    return launch(copy_rows_kernel, dim3((unsigned)(ctas < sms * 4 ? ctas : sms * 4)), 256, a, stream);
+    return launch(copy_rows_kernel, dim3((unsigned)(ctas < sms * 4 ? ctas : sms * 4)), 256, stream, a);
 }
 
 }  // namespace gdn
