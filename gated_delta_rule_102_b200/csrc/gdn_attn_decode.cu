@@ -49,9 +49,6 @@ constexpr int kLaunchRegs = 168;
 #ifndef GDN_ATTN_KU
 #define GDN_ATTN_KU 2
 #endif
-#ifndef GDN_ATTN_NQ
-#define GDN_ATTN_NQ 6
-#endif
 #ifndef GDN_ATTN_SHORT_COST
 #define GDN_ATTN_SHORT_COST 6
 #endif
@@ -65,25 +62,28 @@ constexpr int kShortCost = GDN_ATTN_SHORT_COST, kUnitCost = GDN_ATTN_UNIT_COST; 
 constexpr int kMinShare = GDN_ATTN_MIN_SHARE;  // places of a CTA at least: fewer CTAs, and joins, for little work
 constexpr int kSingle = GDN_ATTN_SINGLE;    // a piece of so many slots or fewer is one token group's alone
 
-// Geometry: D head size, WM row groups of 16 query rows.
+// Geometry: D head size, WM row groups of 16 query rows (0: eight rows).
 template <int D, bool FP8, int WM>
 struct Geo {
     static constexpr int ROWB = D * (FP8 ? 1 : 2);  // bytes of a token's key (value)
     static constexpr int SLOTB = 16 * 1024, HALF = SLOTB / 2;
     static constexpr int ST = HALF / ROWB;          // tokens of a slot
     static constexpr int KU = ST >= 32 ? GDN_ATTN_KU : 1, SUB = KU * 16;  // tokens that a warp works on at a time
-    static constexpr int CS = D == 256 ? 2 : 1;     // column halves
-    static constexpr int ND = D / CS / 8;           // 8-column tiles of a warp's output
-    static constexpr int NG = kComputeWarps / (WM * CS);  // token groups
-    static constexpr int READERS = WM * CS;         // warps that read a slot
-    static constexpr int BM = 16 * WM;
+    static constexpr bool T8 = WM == 0;             // eight rows, transposed products
+    static constexpr int CS = D == 256 && !T8 ? 2 : 1;     // column halves
+    static constexpr int ND = T8 ? D / 16 : D / CS / 8;    // tiles of a warp's output (16 columns by 8 rows, or 8 by 16)
+    static constexpr int READERS = T8 ? 1 : WM * CS;       // warps that read a slot
+    static constexpr int NG = kComputeWarps / READERS;     // token groups
+    static constexpr int BM = T8 ? 8 : 16 * WM;
+    static constexpr int OUTP = 36;                 // (T8) floats of a row of 32 columns on the way out
+    static constexpr int OUTB = T8 ? kComputeWarps * 8 * OUTP * 4 : 0;
     static constexpr int QP = D * 2 + 16;           // bytes from one query row to the next: eight rows, eight bank groups
     static constexpr int QB = BM * QP;
-    static constexpr int NQ = WM == 4 ? 2 : (WM == 2 ? 3 : GDN_ATTN_NQ);  // units whose queries are held
+    static constexpr int NQ = WM == 4 ? 2 : (WM == 2 ? 3 : 6);  // units whose queries are held
     static constexpr int CPR = ROWB / 16;           // 16-byte chunks of a token row
     static constexpr int JOINB = NG == 1 ? 0 : (kComputeWarps / 2) * 32 * ND * 16;
     static constexpr int FIXED = 4096;              // everything small (checked at the launch)
-    static constexpr int FIT = (227 * 1024 - (kAttnMaxBatch + 1) * 4 - FIXED - JOINB - NQ * QB) / SLOTB;
+    static constexpr int FIT = (227 * 1024 - (kAttnMaxBatch + 1) * 4 - FIXED - JOINB - OUTB - NQ * QB) / SLOTB;
     static constexpr int SLOTS = FIT > 12 ? 12 : FIT;
     static_assert(SLOTS >= 8 && ST % SUB == 0 && NG >= 1, "ring");
 };
@@ -95,11 +95,13 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
     using Gm = Geo<D, FP8, WM>;
     constexpr int BM = Gm::BM, ST = Gm::ST, KU = Gm::KU, SUB = Gm::SUB, NG = Gm::NG, CS = Gm::CS, CPR = Gm::CPR, SLOTS = Gm::SLOTS;
     constexpr int NQ = Gm::NQ, QB = Gm::QB, QP = Gm::QP, HALF = Gm::HALF, ND = Gm::ND;
+    constexpr bool T8 = Gm::T8;
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char* ring = smem;
     unsigned char* qbuf = ring + SLOTS * Gm::SLOTB;
     float4* jbuf = reinterpret_cast<float4*>(qbuf + NQ * QB);     // [4 warps][ND][32] joined accumulators
-    float* jm = reinterpret_cast<float*>(qbuf + NQ * QB + Gm::JOINB);  // [4][2][16] their maxima and sums
+    float* obuf = reinterpret_cast<float*>(qbuf + NQ * QB + Gm::JOINB);  // (T8) [8 warps][8][OUTP]
+    float* jm = reinterpret_cast<float*>(qbuf + NQ * QB + Gm::JOINB + Gm::OUTB);  // [4][2][16] their maxima and sums
     float* qexp = jm + 4 * 32;                                    // [NQ][BM] (e4m3) power of two taken out of a query row
     Piece* pieces = reinterpret_cast<Piece*>(qexp + NQ * BM);     // [NQ], then the share's first and last split ones
     uint64_t* full = reinterpret_cast<uint64_t*>(pieces + NQ + 2 + ((NQ + 2) & 1));  // [SLOTS]
@@ -311,8 +313,15 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
     }
 
     // ================= computing =================
-    const int wm = warp % WM, cs = warp / WM % CS, grp = warp / (WM * CS);
+    constexpr int WMX = T8 ? 1 : WM;
+    const int wm = warp % WMX, cs = warp / WMX % CS, grp = warp / (WMX * CS);
     const int g = lane >> 2, j = lane & 3;
+    // A lane's two query rows, and whose element e of an accumulator is: rows g and g + 8 of 16
+    // (elements 0, 1 and 2, 3); or, transposed, rows 2j and 2j + 1 of 8 (even and odd elements).
+    const int ra = T8 ? 2 * j : wm * 16 + g, rb = T8 ? ra + 1 : ra + 8;
+    auto second = [](int e) { return T8 ? (e & 1) : (e >> 1); };
+    // over the lanes that share rows
+    constexpr int XOR0 = T8 ? 4 : 1, XOR1 = T8 ? 32 : 4;
     const bool capped = p.sh.softcap > 0.0f;
     const float qk_scale = p.sh.sm_scale * p.sh.k_scale;
     const float to_log2 = capped ? p.sh.softcap * kLog2e : qk_scale * kLog2e;  // after the cap, or at once
@@ -340,7 +349,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
         const unsigned char* qrow = qbuf + qs * QB;
         const int kv_len = u.past + u.n;
         // row r attends positions lo .. hi-1; every row of the unit those from all_lo to all_hi
-        const int r0 = u.rt * BM + wm * 16 + g, t0 = r0 / G, t1 = (r0 + 8) / G;
+        const int t0 = (u.rt * BM + ra) / G, t1 = (u.rt * BM + rb) / G;
         const int hi0 = min(u.past + t0 + 1, kv_len), hi1 = min(u.past + t1 + 1, kv_len);
         const int lo0 = p.sh.window > 0 ? u.past + t0 + 1 - p.sh.window : 0;
         const int lo1 = p.sh.window > 0 ? u.past + t1 + 1 - p.sh.window : 0;
@@ -348,13 +357,13 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
         // what a product is multiplied by: to log2 units, or to twice the cap's argument
         float f0 = capped ? cap_in : to_log2, f1 = f0;
         if (FP8) {
-            f0 *= qexp[qs * BM + wm * 16 + g];
-            f1 *= qexp[qs * BM + wm * 16 + g + 8];
+            f0 *= qexp[qs * BM + ra];
+            f1 *= qexp[qs * BM + rb];
         }
         float O[ND][4];
 #pragma unroll
         for (int i = 0; i < ND; ++i) O[i][0] = O[i][1] = O[i][2] = O[i][3] = 0.0f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};  // rows g, g + 8: maximum (log2 units), sum
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};  // rows ra, rb: maximum (log2 units), sum
 
         // this group's slots: all of a short piece, in turn with the other groups, or every NG-th
         const bool single = NG == 1 || u.count <= kSingle;
@@ -388,14 +397,51 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                 const bool whole = pos0 >= all_lo && pos0 + SUB <= all_hi;
                 // with few tokens a slot, even and odd steps go to accumulators of their own (a product waits
                 // for the one before it of the same accumulator)
-                constexpr int SETS = KU <= 2 && !FP8 ? 2 : 1;
-                float S[SETS * KU * 2][4];
+                constexpr int NS = T8 ? KU : 2 * KU;  // accumulators of SUB tokens
+                constexpr int SETS = FP8 ? 1 : (T8 && KU == 1 ? 4 : 2);
+                float S[SETS * NS][4];
 #pragma unroll
-                for (int x = 0; x < SETS * KU * 2; ++x) S[x][0] = S[x][1] = S[x][2] = S[x][3] = 0.0f;
-                if (!FP8) {
+                for (int x = 0; x < SETS * NS; ++x) S[x][0] = S[x][1] = S[x][2] = S[x][3] = 0.0f;
+                if (T8) {
+                    // S^T = K Q^T: 16 tokens by 8 rows a product, half of what 16 rows would take
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; kk += 2) {
+                        uint32_t q[4];  // the rows' operands of steps kk and kk + 1
+                        if (!FP8) {
+                            ldsm4(q, qaddr + (lane & 7) * QP + (kk * 2 + (lane >> 3)) * 16);
+                        } else {
+                            const uint2 q0 = *reinterpret_cast<const uint2*>(qrow + g * QP + kk * 32 + j * 8);
+                            const uint2 q1 = *reinterpret_cast<const uint2*>(qrow + g * QP + kk * 32 + 32 + j * 8);
+                            q[0] = q0.x;
+                            q[1] = q0.y;
+                            q[2] = q1.x;
+                            q[3] = q1.y;
+                        }
+#pragma unroll
+                        for (int x = 0; x < KU; ++x) {
+                            if (!FP8) {
+#pragma unroll
+                                for (int y = 0; y < 2; ++y) {
+                                    uint32_t a[4];
+                                    ldsm4(a, ks + chunk_at<CPR>(x * 16 + (lane & 15), (kk + y) * 2 + (lane >> 4)));
+                                    mma<false>(S[(kk + y) % SETS * NS + x], a, q[2 * y], q[2 * y + 1]);
+                                }
+                            } else {
+                                uint32_t v[4];  // tokens 0-7 and 8-15 of chunk kk, then of chunk kk + 1 (see below)
+                                ldsm4(v, ks + chunk_at<CPR>(x * 16 + (lane & 15), kk + (lane >> 4)));
+#pragma unroll
+                                for (int y = 0; y < 2; ++y) {
+                                    const uint32_t a[4] = {e4m3_to_half2(v[2 * y], false), e4m3_to_half2(v[2 * y + 1], false),
+                                                           e4m3_to_half2(v[2 * y], true), e4m3_to_half2(v[2 * y + 1], true)};
+                                    mma<true>(S[x], a, q[2 * y], q[2 * y + 1]);
+                                }
+                            }
+                        }
+                    }
+                } else if (!FP8) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
-                        const int o = SETS == 2 ? (kk & 1) * KU * 2 : 0;
+                        const int o = kk % SETS * NS;
                         uint32_t a[4];
                         ldsm4(a, qaddr + (wm * 16 + (lane & 15)) * QP + (kk * 2 + (lane >> 4)) * 16);
 #pragma unroll
@@ -404,13 +450,6 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                             ldsm4(v, ks + chunk_at<CPR>(x * 16 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)));
                             mma<false>(S[o + 2 * x], a, v[0], v[1]);
                             mma<false>(S[o + 2 * x + 1], a, v[2], v[3]);
-                        }
-                    }
-                    if (SETS == 2) {
-#pragma unroll
-                        for (int x = 0; x < KU * 2; ++x) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) S[x][e] += S[(SETS - 1) * KU * 2 + x][e];
                         }
                     }
                 } else {
@@ -440,41 +479,50 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                         }
                     }
                 }
+#pragma unroll
+                for (int o = 1; o < SETS; ++o) {
+#pragma unroll
+                    for (int x = 0; x < NS; ++x) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) S[x][e] += S[o * NS + x][e];
+                    }
+                }
                 float mx0 = m[0], mx1 = m[1];
                 if (capped) {
 #pragma unroll
-                    for (int x = 0; x < KU * 2; ++x) {
+                    for (int x = 0; x < NS; ++x) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e)  // c tanh(y) = c - 2 c / (1 + e^2y)
-                            S[x][e] = fmaf(-2.0f * to_log2, rcp_fast(1.0f + exp2_fast(S[x][e] * (e < 2 ? f0 : f1))), to_log2);
+                            S[x][e] = fmaf(-2.0f * to_log2, rcp_fast(1.0f + exp2_fast(S[x][e] * (second(e) ? f1 : f0))), to_log2);
                     }
                 } else {
 #pragma unroll
-                    for (int x = 0; x < KU * 2; ++x) {
+                    for (int x = 0; x < NS; ++x) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) S[x][e] *= e < 2 ? f0 : f1;
+                        for (int e = 0; e < 4; ++e) S[x][e] *= second(e) ? f1 : f0;
                     }
                 }
                 if (!whole) {
 #pragma unroll
-                    for (int x = 0; x < KU * 2; ++x) {
+                    for (int x = 0; x < NS; ++x) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int pos = pos0 + x * 8 + 2 * j + (e & 1);
-                            const bool in = e < 2 ? pos < hi0 && pos >= lo0 : pos < hi1 && pos >= lo1;
+                            const int pos = pos0 + (T8 ? x * 16 + g + (e >> 1) * 8 : x * 8 + 2 * j + (e & 1));
+                            const bool in = second(e) ? pos < hi1 && pos >= lo1 : pos < hi0 && pos >= lo0;
                             S[x][e] = in ? S[x][e] : -INFINITY;
                         }
                     }
                 }
 #pragma unroll
-                for (int x = 0; x < KU * 2; ++x) {
-                    mx0 = fmaxf(mx0, fmaxf(S[x][0], S[x][1]));
-                    mx1 = fmaxf(mx1, fmaxf(S[x][2], S[x][3]));
+                for (int x = 0; x < NS; ++x) {
+                    mx0 = fmaxf(mx0, T8 ? fmaxf(S[x][0], S[x][2]) : fmaxf(S[x][0], S[x][1]));
+                    mx1 = fmaxf(mx1, T8 ? fmaxf(S[x][1], S[x][3]) : fmaxf(S[x][2], S[x][3]));
                 }
-                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+#pragma unroll
+                for (int o = XOR0; o < XOR1; o <<= 1) {
+                    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+                    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+                }
                 const float ref0 = mx0 == -INFINITY ? 0.0f : mx0, ref1 = mx1 == -INFINITY ? 0.0f : mx1;  // nothing seen yet
                 if (__any_sync(0xffffffffu, mx0 != m[0] || mx1 != m[1])) {
                     const float a0 = exp2_fast(m[0] - ref0), a1 = exp2_fast(m[1] - ref1);
@@ -482,20 +530,18 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                     l[1] *= a1;
 #pragma unroll
                     for (int x = 0; x < ND; ++x) {
-                        O[x][0] *= a0;
-                        O[x][1] *= a0;
-                        O[x][2] *= a1;
-                        O[x][3] *= a1;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) O[x][e] *= second(e) ? a1 : a0;
                     }
                     m[0] = mx0;
                     m[1] = mx1;
                 }
 #pragma unroll
-                for (int x = 0; x < KU * 2; ++x) {
+                for (int x = 0; x < NS; ++x) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        S[x][e] = exp2_fast(S[x][e] - (e < 2 ? ref0 : ref1));
-                        l[e >> 1] += S[x][e];
+                        S[x][e] = exp2_fast(S[x][e] - (second(e) ? ref1 : ref0));
+                        l[second(e)] += S[x][e];
                     }
                 }
 
@@ -515,7 +561,37 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                     }
                     plain = !__any_sync(0xffffffffu, bad);
                 }
-                if (plain) {
+                if (plain && T8) {
+                    // O^T += V^T P^T: 16 columns by 8 rows a product; the probabilities' operand is their
+                    // accumulator transposed
+#pragma unroll
+                    for (int x = 0; x < KU; ++x) {
+                        const uint32_t b0 = transpose8(pack2<FP8>(S[x][0], S[x][1])), b1 = transpose8(pack2<FP8>(S[x][2], S[x][3]));
+                        if (!FP8) {
+#pragma unroll
+                            for (int c = 0; c < ND; ++c) {
+                                uint32_t a[4];
+                                ldsm4t(a, vs + chunk_at<CPR>(x * 16 + (lane & 7) + ((lane >> 4) << 3), c * 2 + ((lane >> 3) & 1)));
+                                mma<false>(O[c], a, b0, b1);
+                            }
+                        } else {
+                            // rows g of the operand take the even columns of chunk c, rows g + 8 the odd ones
+#pragma unroll
+                            for (int c = 0; c < ND; c += 2) {
+                                uint32_t v[4];
+                                ldsm4t(v, vs + chunk_at<CPR>(x * 16 + (lane & 15), c + (lane >> 4)));
+#pragma unroll
+                                for (int y = 0; y < 2; ++y) {
+                                    const uint32_t x0 = e4m3_to_half2(v[2 * y], false), y0 = e4m3_to_half2(v[2 * y], true);
+                                    const uint32_t x1 = e4m3_to_half2(v[2 * y + 1], false), y1 = e4m3_to_half2(v[2 * y + 1], true);
+                                    const uint32_t a[4] = {__byte_perm(x0, y0, 0x5410), __byte_perm(x0, y0, 0x7632),
+                                                           __byte_perm(x1, y1, 0x5410), __byte_perm(x1, y1, 0x7632)};
+                                    mma<true>(O[c + y], a, b0, b1);
+                                }
+                            }
+                        }
+                    }
+                } else if (plain) {
 #pragma unroll
                     for (int x = 0; x < KU; ++x) {
                         const uint32_t a[4] = {pack2<FP8>(S[2 * x][0], S[2 * x][1]), pack2<FP8>(S[2 * x][2], S[2 * x][3]),
@@ -551,30 +627,36 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                     for (int t = 0; t < SUB; ++t) {
                         uint32_t b0 = 0, b1 = 0;  // by masks: an index known at run time only would put S into local memory
 #pragma unroll
-                        for (int x = 0; x < KU * 2; ++x) {
-                            const uint32_t even = x == (t >> 3) && !(t & 1) ? ~0u : 0u, odd = x == (t >> 3) && (t & 1) ? ~0u : 0u;
-                            b0 |= (__float_as_uint(S[x][0]) & even) | (__float_as_uint(S[x][1]) & odd);
-                            b1 |= (__float_as_uint(S[x][2]) & even) | (__float_as_uint(S[x][3]) & odd);
+                        for (int x = 0; x < NS; ++x) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {  // this lane's elements of token t, if it has them
+                                uint32_t mask = (T8 ? x == (t >> 4) && (e >> 1) == ((t >> 3) & 1) : x == (t >> 3) && (e & 1) == (t & 1)) ? ~0u : 0u;
+                                asm("" : "+r"(mask));  // (or the compiler makes an index of it after all)
+                                const uint32_t bits = __float_as_uint(S[x][e]) & mask;
+                                if (second(e)) b1 |= bits; else b0 |= bits;
+                            }
                         }
-                        const float p0 = __uint_as_float(__shfl_sync(0xffffffffu, b0, (lane & ~3) | ((t >> 1) & 3)));
-                        const float p1 = __uint_as_float(__shfl_sync(0xffffffffu, b1, (lane & ~3) | ((t >> 1) & 3)));
+                        const int holder = T8 ? (t & 7) * 4 + j : (lane & ~3) | ((t >> 1) & 3);
+                        const float p0 = __uint_as_float(__shfl_sync(0xffffffffu, b0, holder));
+                        const float p1 = __uint_as_float(__shfl_sync(0xffffffffu, b1, holder));
                         const int pos = pos0 + t;
                         const bool in0 = pos < hi0 && pos >= lo0, in1 = pos < hi1 && pos >= lo1;
 #pragma unroll
                         for (int x = 0; x < ND; ++x) {
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
+                            for (int e = 0; e < 2; ++e) {  // the lane's two columns of tile x
                                 float v;
                                 if (!FP8) {
-                                    const int col = cs * (ND * 8) + x * 8 + 2 * j + e;
+                                    const int col = T8 ? x * 16 + g + 8 * e : cs * (ND * 8) + x * 8 + 2 * j + e;
                                     v = bf16_bits_to_float(*reinterpret_cast<const uint16_t*>(kt + HALF + chunk_at<CPR>(t, col >> 3) + (col & 7) * 2));
                                 } else {
-                                    const int col = cs * (ND * 8) + (x >> 1) * 16 + 4 * j + 2 * e + (x & 1);
+                                    const int col = T8 ? x * 16 + 2 * g + e : cs * (ND * 8) + (x >> 1) * 16 + 4 * j + 2 * e + (x & 1);
                                     const uint32_t hh = e4m3_to_half2(*(kt + HALF + chunk_at<CPR>(t, col >> 4) + (col & 15)), false);
                                     v = __low2float(*reinterpret_cast<const __half2*>(&hh));
                                 }
-                                if (in0) O[x][e] = fmaf(p0, v, O[x][e]);
-                                if (in1) O[x][e + 2] = fmaf(p1, v, O[x][e + 2]);
+                                const int ea = T8 ? 2 * e : e, eb = T8 ? 2 * e + 1 : e + 2;
+                                if (in0) O[x][ea] = fmaf(p0, v, O[x][ea]);
+                                if (in1) O[x][eb] = fmaf(p1, v, O[x][eb]);
                             }
                         }
                     }
@@ -589,8 +671,8 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
         if (lane == 0) add_release(qfreed + qs);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+#pragma unroll
+            for (int o = XOR0; o < XOR1; o <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
         }
 
         // ---- the token groups joined, half of them into the other half, down to group 0 ----
@@ -605,31 +687,30 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                 if (grp >= half && grp < 2 * half) {
 #pragma unroll
                     for (int x = 0; x < ND; ++x) at[x * 32] = make_float4(O[x][0], O[x][1], O[x][2], O[x][3]);
-                    if (j == 0) {
-                        jr[g] = m[0];
-                        jr[g + 8] = m[1];
-                        jr[16 + g] = l[0];
-                        jr[24 + g] = l[1];
+                    if (T8 ? g == 0 : j == 0) {
+                        jr[ra & 15] = m[0];
+                        jr[rb & 15] = m[1];
+                        jr[16 + (ra & 15)] = l[0];
+                        jr[16 + (rb & 15)] = l[1];
                     }
                 }
                 if (!meet()) return;
                 if (grp < half) {
-                    const float om0 = jr[g], om1 = jr[g + 8];
+                    const float om0 = jr[ra & 15], om1 = jr[rb & 15];
                     const float n0 = fmaxf(m[0], om0), n1 = fmaxf(m[1], om1);
                     const float z0 = n0 == -INFINITY ? 0.0f : n0, z1 = n1 == -INFINITY ? 0.0f : n1;
                     const float a0 = exp2_fast(m[0] - z0), a1 = exp2_fast(m[1] - z1);
                     const float b0 = exp2_fast(om0 - z0), b1 = exp2_fast(om1 - z1);
-                    l[0] = l[0] * a0 + jr[16 + g] * b0;
-                    l[1] = l[1] * a1 + jr[24 + g] * b1;
+                    l[0] = l[0] * a0 + jr[16 + (ra & 15)] * b0;
+                    l[1] = l[1] * a1 + jr[16 + (rb & 15)] * b1;
                     m[0] = n0;
                     m[1] = n1;
 #pragma unroll
                     for (int x = 0; x < ND; ++x) {
                         const float4 o = at[x * 32];
-                        O[x][0] = O[x][0] * a0 + o.x * b0;
-                        O[x][1] = O[x][1] * a0 + o.y * b0;
-                        O[x][2] = O[x][2] * a1 + o.z * b1;
-                        O[x][3] = O[x][3] * a1 + o.w * b1;
+                        const float other[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) O[x][e] = O[x][e] * (second(e) ? a1 : a0) + other[e] * (second(e) ? b1 : b0);
                     }
                 }
             }
@@ -644,8 +725,64 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
             if (which) split_last = true; else split_first = true;
             if (warp == 0 && lane == 0) pieces[NQ + which] = u;
         }
-        if (grp == owner) {
-            const int a = wm * 16 + g;
+        if (T8 && grp == owner) {
+            // 32 columns at a time through this warp's part of shared memory, rows by rows: a lane holds
+            // columns of two rows, but eight lanes write a row together
+            float* mine = p.partial + (size_t)(blockIdx.x * 2 + ((int)blockIdx.x == u.c0)) * PSTRIDE;
+            float* mem = obuf + warp * (8 * Gm::OUTP);
+            const float inv0 = p.sh.v_scale / l[0], inv1 = p.sh.v_scale / l[1];
+            uint2 z[D / 32][2];
+            float inv[2];
+            int head[2];
+            size_t row[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int r = y * 4 + (lane >> 3), rr = u.rt * BM + r, t = rr / G;
+                const float a = __shfl_sync(0xffffffffu, inv0, r >> 1), b = __shfl_sync(0xffffffffu, inv1, r >> 1);
+                inv[y] = (r & 1) ? b : a;
+                head[y] = u.h * G + rr - t * G;
+                row[y] = (size_t)u.first + t;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c)
+                    z[c][y] = !split && p.gate.ptr && r < rows ? gate_of4(p, row[y], head[y], c * 32 + (lane & 7) * 4) : make_uint2(0, 0);
+            }
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                __syncwarp();
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int col = x * 16 + (FP8 ? 2 * g + (e >> 1) : g + 8 * (e >> 1));
+                        mem[(2 * j + (e & 1)) * Gm::OUTP + col] = O[c * 2 + x][e];
+                    }
+                }
+                __syncwarp();
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int r = y * 4 + (lane >> 3), col = c * 32 + (lane & 7) * 4;
+                    const float4 o = *reinterpret_cast<const float4*>(mem + r * Gm::OUTP + (lane & 7) * 4);
+                    if (r >= rows) continue;
+                    if (split) *reinterpret_cast<float4*>(mine + r * D + col) = o;
+                    else write_out4(p, row[y], head[y], D, col, o, inv[y], z[c][y]);
+                }
+            }
+            if (g == 0) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 2 * j + e, rr = u.rt * BM + r, t = rr / G;
+                    if (r >= rows) continue;
+                    if (split) {
+                        mine[BM * D + r] = m[e];
+                        mine[BM * D + BM + r] = l[e];
+                    } else if (p.lse) {
+                        p.lse[((size_t)u.first + t) * p.sh.Hq + u.h * G + rr - t * G] = (m[e] + log2f(l[e])) * kLn2;
+                    }
+                }
+            }
+        }
+        if (!T8 && grp == owner) {
+            const int a = wm * 16 + g, r0 = u.rt * BM + a;
             const bool in0 = a < rows, in1 = a + 8 < rows;
             if (split) {
                 float* mine = p.partial + (size_t)(blockIdx.x * 2 + ((int)blockIdx.x == u.c0)) * PSTRIDE;
@@ -731,7 +868,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
     int dev, sms;
     cudaError_t e = device_sms(&dev, &sms);
     if (e != cudaSuccess) return e;
-    const size_t smem = Gm::SLOTS * (size_t)Gm::SLOTB + Gm::NQ * (size_t)Gm::QB + Gm::JOINB + Gm::FIXED + ((size_t)a.B + 1) * 4;
+    const size_t smem = Gm::SLOTS * (size_t)Gm::SLOTB + Gm::NQ * (size_t)Gm::QB + Gm::JOINB + Gm::OUTB + Gm::FIXED + ((size_t)a.B + 1) * 4;
     static_assert(4 * 32 * 4 + Gm::NQ * Gm::BM * 4 + (Gm::NQ + 3) * (int)sizeof(Piece) + (Gm::SLOTS + Gm::NQ + 1) * 8 +
                       (Gm::SLOTS + Gm::NQ + 16) * 4 <= Gm::FIXED, "small data");
     static std::once_flag once[kMaxDevices];
@@ -764,12 +901,13 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, kern, a, map_k, map_v, box);
 }
 
-// Row groups for `rows` query rows per key/value head.
-int row_groups(int rows) { return rows <= 16 ? 1 : (rows <= 32 ? 2 : 4); }
+// Row groups for `rows` query rows per key/value head (0: up to eight rows, transposed).
+int row_groups(int rows) { return rows <= 8 ? 0 : (rows <= 16 ? 1 : (rows <= 32 ? 2 : 4)); }
 
 template <int D, bool FP8>
 cudaError_t launch_rows(const AttnArgs& a, cudaStream_t stream) {
     switch (row_groups(a.T * a.sh.G)) {
+        case 0: return launch<D, FP8, 0>(a, stream);
         case 1: return launch<D, FP8, 1>(a, stream);
         case 2: return launch<D, FP8, 2>(a, stream);
         default: return launch<D, FP8, 4>(a, stream);
@@ -779,7 +917,7 @@ cudaError_t launch_rows(const AttnArgs& a, cudaStream_t stream) {
 }  // namespace
 
 size_t attn_workspace_bytes(int d, bool fp8, int page_size, int rows) {
-    const int tile = attn_rows_supported(fp8, page_size, rows) ? 128 : 16 * row_groups(rows);
+    const int tile = attn_rows_supported(fp8, page_size, rows) ? 128 : 16 * (row_groups(rows) ? row_groups(rows) : 1);
     return kAttnPartialAt + (size_t)kAttnMaxCtas * 2 * tile * (d + 2) * sizeof(float);
 }
 

@@ -327,9 +327,9 @@ __global__ void __launch_bounds__(256) pages_renumber_kernel(const PageArgs p) {
 // all loaded before the first store); with 32 warps an SM keeps 128 KB in flight, above
 // what latency times bandwidth needs (about 45 KB), and rows of any size, one page or a
 // 2 MB state, spread over the whole GPU. Bound by HBM: each byte is read and written once.
-constexpr int kPiece = 4096;
+constexpr int kWords = 8, kPiece = kWords * 512, kCtas = 4;
 
-__global__ void __launch_bounds__(256, 4) copy_rows_kernel(const __grid_constant__ CopyArgs p) {
+__global__ void __launch_bounds__(256, kCtas) copy_rows_kernel(const __grid_constant__ CopyArgs p) {
     pdl_wait();
     int n = p.n_max;
     if (p.n_dev) {
@@ -359,12 +359,12 @@ __global__ void __launch_bounds__(256, 4) copy_rows_kernel(const __grid_constant
         const int words = (int)((bytes - at < kPiece ? bytes - at : kPiece) / 16);
         const uint4* s = reinterpret_cast<const uint4*>(p.base[lo] + src * bytes + at);
         uint4* d = reinterpret_cast<uint4*>(p.base[lo] + dst * bytes + at);
-        uint4 w[8];
+        uint4 w[kWords];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < kWords; ++i)
             if (lane + 32 * i < words) w[i] = __ldcs(s + lane + 32 * i);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < kWords; ++i)
             if (lane + 32 * i < words) __stcs(d + lane + 32 * i, w[i]);
     }
 }
@@ -427,7 +427,7 @@ cudaError_t launch_copy_rows(CopyArgs& a, cudaStream_t stream) {
     }
     a.first_chunk[a.n_bufs] = chunks;
     const long ctas = (chunks * a.n_max + 7) / 8;
-    return launch(copy_rows_kernel, dim3((unsigned)(ctas < sms * 4 ? ctas : sms * 4)), 256, stream, a);
+    return launch(copy_rows_kernel, dim3((unsigned)(ctas < sms * kCtas ? ctas : sms * kCtas)), 256, stream, a);
 }
 
 }  // namespace gdn
