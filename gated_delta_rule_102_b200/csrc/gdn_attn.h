@@ -126,9 +126,10 @@ struct CopyArgs {
 };
 cudaError_t launch_copy_rows(CopyArgs& a, cudaStream_t stream);
 
-// A tiled tensor map of bf16 values or bytes, swizzled over its inner dimension of 128 or 64 bytes.
+// A tiled tensor map of bf16 values or bytes, swizzled over its inner dimension of 128 or 64 bytes;
+// wide: misses in L2 fetch 256 bytes (128 otherwise).
 bool encode_tensor_map(CUtensorMap* m, bool bytes, int rank, void* ptr, const cuuint64_t* dims, const cuuint64_t* strides,
-                       const cuuint32_t* box, int inner_bytes);
+                       const cuuint32_t* box, int inner_bytes, bool wide);
 
 // The number of SMs of the current device (looked up once per device).
 cudaError_t device_sms(int* device, int* sms);

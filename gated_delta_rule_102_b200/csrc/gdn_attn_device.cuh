@@ -442,7 +442,9 @@ inline bool make_pool_map(CUtensorMap* m, void* pool, const AttnArgs& a, int row
                                 (cuuint64_t)a.sh.Hkv};
     const cuuint64_t strides[4] = {token, (cuuint64_t)inner, token * 8, (cuuint64_t)row_bytes};
     const cuuint32_t boxes[5] = {(cuuint32_t)(inner / esz), 8, (cuuint32_t)blocks, (cuuint32_t)box / 8, 1};
-    return encode_tensor_map(m, a.sh.fp8, 5, pool, dims, strides, boxes, inner);
+    // A token's row of a head that is 128 bytes long lies alone: fetching 256 would bring another head's,
+    // too (d = 64 bf16, 64 x 6700 tokens: 223 us, 177 with 128).
+    return encode_tensor_map(m, a.sh.fp8, 5, pool, dims, strides, boxes, inner, row_bytes >= 256);
 }
 
 }  // namespace gdn

@@ -11,7 +11,7 @@
 // owns a row (no shuffles); P goes to shared memory as bf16 and O (128 x d, fp32) stays in
 // TMEM. O is rescaled only when a row's maximum has grown by more than 2^8 since the last
 // time (P and the sums stay within range until then, and the quotient is the same).
-// Warps: four of softmax, one issues the products, one loads tiles by TMA.
+// Warps: four of softmax, one issues the products, three load keys, values and queries by TMA.
 //
 // Bound: a tile of 64 tokens at d = 256 is 64 KB of HBM, about 2700 cycles of an SM's share;
 // its products take about 1000 and the softmax of 128 rows about 1500.
@@ -153,33 +153,28 @@ attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUt
         at.tile = 0;
     };
 
-    if (warp == 5) {
-        // ================= loading: tile n's keys and values =================
+    if (warp == 5 || warp == 7) {
+        // ================= loading: tile n's keys, or values =================
+        // (a warp each: values are held until the softmax is done, keys are not, and neither waits for
+        // the other's place)
+        const bool v = warp == 7;
+        uint64_t *full = v ? vfull : kfull, *empty = v ? vempty : kempty;
+        unsigned char* ring = v ? vring : kring;
+        const CUtensorMap* map = v ? &map_v : &map_k;
         const int x = lane * box < kTile ? lane : -1;  // this lane's part of a tile
-        int n = 0, issued[2] = {0, 0};
-        bool more = true;
-        while (more) {
+        int n = 0;
+        for (bool more = true; more; ++n) {
             const int st = n % SLOTS, turn = n / SLOTS, h = at.unit % Hkv;
             const int tok = x >= 0 ? at.look_up(at.s.base + at.tile * kTile + x * box, box) : -1;
             const unsigned bytes = __popc(__ballot_sync(0xffffffffu, tok >= 0)) * box * D * 2;
-            bool ok = true;
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                uint64_t* full = (v ? vfull : kfull) + st;
-                if (turn > 0 && !(ok = wait((v ? vempty : kempty) + st, (turn - 1) & 1))) break;
-                if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-                __syncwarp();
-                if (tok >= 0) tma_load_5d(smem_addr((v ? vring : kring) + st * TILEB) + x * box * D * 2, v ? &map_v : &map_k, tok >> 3, h, smem_addr(full));
-                ++issued[v];
-            }
-            if (!ok) break;
-            ++n;
+            if (turn > 0 && !wait(empty + st, (turn - 1) & 1)) break;
+            if (lane == 0) mbar_arrive_expect_tx(full + st, bytes);
+            __syncwarp();
+            if (tok >= 0) tma_load_5d(smem_addr(ring + st * TILEB) + x * box * D * 2, map, tok >> 3, h, smem_addr(full + st));
             more = at.advance(1);
         }
         // what is still in flight lands before the block leaves (all of it has, unless a wait ran out)
-        for (int v = 0; v < 2; ++v) {
-            for (int i = max(0, issued[v] - SLOTS); i < issued[v]; ++i) mbar_wait_bounded((v ? vfull : kfull) + i % SLOTS, (i / SLOTS) & 1);
-        }
+        for (int i = max(0, n - SLOTS); i < n; ++i) mbar_wait_bounded(full + i % SLOTS, (i / SLOTS) & 1);
     } else if (warp == 4) {
         // ================= products: one thread =================
         if (lane == 0) {
@@ -571,7 +566,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
         const cuuint64_t dims[4] = {64, (cuuint64_t)a.sh.Hq, (cuuint64_t)a.total, (cuuint64_t)Gm::NB};
         const cuuint64_t strides[3] = {(cuuint64_t)(a.q.head ? a.q.head * 2 : 16), (cuuint64_t)(a.q.row ? a.q.row * 2 : 16), 128};
         const cuuint32_t boxes[4] = {64, (cuuint32_t)a.sh.G, (cuuint32_t)q_tokens, 1};
-        if (!encode_tensor_map(&map_q, false, 4, const_cast<uint16_t*>(a.q.ptr), dims, strides, boxes, 128)) return cudaErrorInvalidValue;
+        if (!encode_tensor_map(&map_q, false, 4, const_cast<uint16_t*>(a.q.ptr), dims, strides, boxes, 128, true)) return cudaErrorInvalidValue;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(sms < kAttnMaxCtas ? sms : kAttnMaxCtas));

@@ -289,13 +289,13 @@ bool make_map(CUtensorMap* m, const void* ptr, int rows, int cols, int box_rows)
 }  // namespace
 
 bool encode_tensor_map(CUtensorMap* m, bool bytes, int rank, void* ptr, const cuuint64_t* dims, const cuuint64_t* strides,
-                       const cuuint32_t* box, int inner_bytes) {
+                       const cuuint32_t* box, int inner_bytes, bool wide) {
     auto fn = encode_fn();
     if (!fn) return false;
     const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
     return fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, ptr, dims, strides,
               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, inner_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              wide ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The kernel's dynamic shared-memory limit, raised once per device to what the largest
