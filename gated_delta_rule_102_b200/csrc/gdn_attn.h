@@ -78,16 +78,12 @@ constexpr int kAttnMaxCtas = 192;
 constexpr int kAttnCounters = 3 * kAttnMaxCtas;  // arrivals at units, and at groups of their pieces
 constexpr size_t kAttnPartialAt = kAttnCounters * sizeof(unsigned int) + kAttnMaxCtas * sizeof(Piece);  // workspace offset
 constexpr int kAttnMaxBatch = 2048;
-#ifndef GDN_ATTN_FEW
-#define GDN_ATTN_FEW 16
-#endif
-constexpr int kAttnFewRows = GDN_ATTN_FEW;  // query rows per key/value head that the kernel for few rows takes in any case
 size_t attn_workspace_bytes(int d, bool fp8, int page_size, int rows);
 
 cudaError_t launch_qk_rope_append(const AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t stream);
 // The kernel for many rows on the tensor cores: whether it takes the shape, and its launch.
-bool attn_rows_supported(bool fp8, int page_size, int rows);
+bool attn_rows_supported(int d, bool fp8, int page_size, int rows);
 cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t stream);
 
 struct PageArgs {

@@ -194,7 +194,7 @@ gdn_status gdn_attn_decode(const gdn_attn_config* cfg, const gdn_kv_cache* cache
     // (a broadcast row or head, stride 0, has no tensor map: the kernel for few rows takes it, whose
     // partial results are smaller)
     const bool broadcast = (a.q.row == 0 && total_tokens > 1) || (a.q.head == 0 && a.sh.Hq > 1);
-    const bool many = gdn::attn_rows_supported(a.sh.fp8, a.sh.page_size, rows) && !broadcast;
+    const bool many = gdn::attn_rows_supported(a.sh.d, a.sh.fp8, a.sh.page_size, rows) && !broadcast;
     return from_cuda(many ? gdn::launch_attn_rows(a, (cudaStream_t)stream) : gdn::launch_attn_decode(a, (cudaStream_t)stream));
 }
 

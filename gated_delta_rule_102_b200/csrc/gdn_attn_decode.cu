@@ -43,24 +43,13 @@ namespace {
 
 constexpr int kLoadWarps = 3, kComputeWarps = 8, kAttnThreads = (kLoadWarps + 1 + kComputeWarps) * 32;
 constexpr int kLaunchRegs = 168;
-#ifndef GDN_ATTN_UNIT_COST
-#define GDN_ATTN_UNIT_COST 12
-#endif
-#ifndef GDN_ATTN_KU
-#define GDN_ATTN_KU 2
-#endif
-#ifndef GDN_ATTN_SHORT_COST
-#define GDN_ATTN_SHORT_COST 6
-#endif
-#ifndef GDN_ATTN_SINGLE
-#define GDN_ATTN_SINGLE 4
-#endif
-#ifndef GDN_ATTN_MIN_SHARE
-#define GDN_ATTN_MIN_SHARE 8
-#endif
-constexpr int kShortCost = GDN_ATTN_SHORT_COST, kUnitCost = GDN_ATTN_UNIT_COST;  // what a unit costs beside its slots, in slots (its queries, the join, the output)
-constexpr int kMinShare = GDN_ATTN_MIN_SHARE;  // places of a CTA at least: fewer CTAs, and joins, for little work
-constexpr int kSingle = GDN_ATTN_SINGLE;    // a piece of so many slots or fewer is one token group's alone
+// What a unit costs beside its slots, in slots: its queries, the join of the token groups, the
+// output. Measured as a whole: with 4 for every unit 256 sequences of 500 to 16000 tokens take 383
+// us, with 12 for the longer ones 360; a mix of many short ones takes 80 with 12 for all, 62 with
+// 6 for the short ones.
+constexpr int kShortCost = 6, kUnitCost = 12;
+constexpr int kSingle = 4;    // a piece of so many slots or fewer is one token group's alone (1: 79 us instead of 68 at 16 to 300 tokens)
+constexpr int kMinShare = 8;  // places of a CTA at least: fewer CTAs, and joins, for little work
 
 // Geometry: D head size, WM row groups of 16 query rows (0: eight rows).
 template <int D, bool FP8, int WM>
@@ -68,7 +57,7 @@ struct Geo {
     static constexpr int ROWB = D * (FP8 ? 1 : 2);  // bytes of a token's key (value)
     static constexpr int SLOTB = 16 * 1024, HALF = SLOTB / 2;
     static constexpr int ST = HALF / ROWB;          // tokens of a slot
-    static constexpr int KU = ST >= 32 ? GDN_ATTN_KU : 1, SUB = KU * 16;  // tokens that a warp works on at a time
+    static constexpr int KU = ST >= 32 ? 2 : 1, SUB = KU * 16;  // tokens that a warp works on at a time
     static constexpr bool T8 = WM == 0;             // eight rows, transposed products
     static constexpr int CS = D == 256 && !T8 ? 2 : 1;     // column halves
     static constexpr int ND = T8 ? D / 16 : D / CS / 8;    // tiles of a warp's output (16 columns by 8 rows, or 8 by 16)
@@ -917,7 +906,7 @@ cudaError_t launch_rows(const AttnArgs& a, cudaStream_t stream) {
 }  // namespace
 
 size_t attn_workspace_bytes(int d, bool fp8, int page_size, int rows) {
-    const int tile = attn_rows_supported(fp8, page_size, rows) ? 128 : 16 * (row_groups(rows) ? row_groups(rows) : 1);
+    const int tile = attn_rows_supported(d, fp8, page_size, rows) ? 128 : 16 * (row_groups(rows) ? row_groups(rows) : 1);
     return kAttnPartialAt + (size_t)kAttnMaxCtas * 2 * tile * (d + 2) * sizeof(float);
 }
 

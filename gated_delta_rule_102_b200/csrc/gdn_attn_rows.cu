@@ -28,14 +28,8 @@ namespace gdn {
 namespace {
 
 constexpr int kTile = 64, kRowTile = 128, kThreads = 256, kSoftmaxWarps = 4;
-#ifndef GDN_ROWS_COST
-#define GDN_ROWS_COST 4
-#endif
-#ifndef GDN_ROWS_MIN_SHARE
-#define GDN_ROWS_MIN_SHARE 8
-#endif
-constexpr int kCost = GDN_ROWS_COST;           // places of a unit beside its tiles'
-constexpr int kMinShare = GDN_ROWS_MIN_SHARE;  // places of a CTA at least
+constexpr int kCost = 4;       // places of a unit beside its tiles'
+constexpr int kMinShare = 8;   // places of a CTA at least
 constexpr float kRescale = 8.0f;               // growth of a row's maximum (log2) that makes it the new reference
 
 template <int D>
@@ -586,9 +580,15 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-// Rows per key/value head from which this kernel is the faster one (see the comment at the
-// launch of the other).
-bool attn_rows_supported(bool fp8, int page_size, int rows) { return !fp8 && page_size % 8 == 0 && rows > kAttnFewRows; }
+// The rows per key/value head from which this kernel is the faster one on long contexts. Its time
+// hardly depends on them, the other kernel's does (two key/value heads, 64 sequences of 2000 to
+// 8000 tokens, us, this | other): d = 256: 32 rows 133 | 171, 64 rows 137 | 317; d = 128: 32 rows
+// 97 | 67, 64 rows 99 | 108; d = 64: 32 rows 82 | 48, 64 rows 82 | 78. (At 100 to 800 tokens, 8
+// sequences, the other one is ahead by 3 to 12 us throughout; the host does not know the lengths.)
+bool attn_rows_supported(int d, bool fp8, int page_size, int rows) {
+    const int few = d == 256 ? 16 : (d == 128 ? 32 : 64);
+    return !fp8 && page_size % 8 == 0 && rows > few;
+}
 
 cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t stream) {
     switch (a.sh.d) {
