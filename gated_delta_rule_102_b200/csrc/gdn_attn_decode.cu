@@ -70,7 +70,11 @@ struct Geo {
     static constexpr int QB = BM * QP;
     static constexpr int NQ = WM == 4 ? 2 : (WM == 2 ? 3 : 6);  // units whose queries are held
     static constexpr int CPR = ROWB / 16;           // 16-byte chunks of a token row
-    static constexpr int JOINB = NG == 1 ? 0 : (kComputeWarps / 2) * 32 * ND * 16;
+    // The join of the token groups, so many columns of every group's output at a time, in rows that
+    // spread a warp's stores over the banks.
+    static constexpr int ROUNDS = ND > 8 ? ND / 8 : 1, RND = ND / ROUNDS;
+    static constexpr int WCOLS = RND * (T8 ? 16 : 8), COLS = WCOLS * CS, JPITCH = COLS + (T8 ? 4 : (FP8 ? 16 : 8));
+    static constexpr int JOINB = NG == 1 ? 0 : NG * BM * JPITCH * 4;
     static constexpr int FIXED = 4096;              // everything small (checked at the launch)
     static constexpr int FIT = (227 * 1024 - (kAttnMaxBatch + 1) * 4 - FIXED - JOINB - OUTB - NQ * QB) / SLOTB;
     static constexpr int SLOTS = FIT > 12 ? 12 : FIT;
@@ -88,17 +92,18 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char* ring = smem;
     unsigned char* qbuf = ring + SLOTS * Gm::SLOTB;
-    float4* jbuf = reinterpret_cast<float4*>(qbuf + NQ * QB);     // [4 warps][ND][32] joined accumulators
+    float* jbuf = reinterpret_cast<float*>(qbuf + NQ * QB);       // [NG][BM][JPITCH] outputs to be joined
     float* obuf = reinterpret_cast<float*>(qbuf + NQ * QB + Gm::JOINB);  // (T8) [8 warps][8][OUTP]
-    float* jm = reinterpret_cast<float*>(qbuf + NQ * QB + Gm::JOINB + Gm::OUTB);  // [4][2][16] their maxima and sums
-    float* qexp = jm + 4 * 32;                                    // [NQ][BM] (e4m3) power of two taken out of a query row
+    float* jm = reinterpret_cast<float*>(qbuf + NQ * QB + Gm::JOINB + Gm::OUTB);  // [NG][2][BM] their maxima and sums
+    float* qexp = jm + NG * 2 * BM;                                   // [NQ][BM] (e4m3) power of two taken out of a query row
     Piece* pieces = reinterpret_cast<Piece*>(qexp + NQ * BM);     // [NQ], then the share's first and last split ones
     uint64_t* full = reinterpret_cast<uint64_t*>(pieces + NQ + 2 + ((NQ + 2) & 1));  // [SLOTS]
     uint64_t* qfull = full + SLOTS;                               // [NQ]
     uint64_t* cbar = qfull + NQ;                                  // the computing warps' barrier
     // Releases are counted, not phased: a warp comes back to a place only every few turns, and
     // a barrier's phase parity cannot tell a turn from the one two before it.
-    int* freed = reinterpret_cast<int*>(cbar + 1);                // [SLOTS] warps that are done with a slot, all turns
+    uint64_t* rbar = cbar + 1;                                    // their reads of the last join
+    int* freed = reinterpret_cast<int*>(rbar + 1);                // [SLOTS] warps that are done with a slot, all turns
     int* qfreed = freed + SLOTS;                                  // [NQ] the same for a unit's queries
     int* misc = qfreed + NQ;                                      // [16] sums of the schedule's warps; 12: last to arrive; 15: stop
     int* prefix = misc + 16;                                      // [B + 1] cost of the sequences before each
@@ -116,6 +121,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
             qfreed[i] = 0;
         }
         mbar_init(cbar, kComputeWarps);
+        mbar_init(rbar, kComputeWarps);
         *stop = 0;
         if (box) {
             asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&map_k)) : "memory");
@@ -328,7 +334,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
     bool split_first = false, split_last = false;
 
     bool last = false;
-    for (int done = 0, ord = 0; !last; ++ord) {
+    for (int done = 0, ord = 0, joins = 0; !last; ++ord) {
         const int qs = ord % NQ;
         if (!wait(qfull + qs, (ord / NQ) & 1)) return;
         const Piece u = pieces[qs];
@@ -356,7 +362,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
 
         // this group's slots: all of a short piece, in turn with the other groups, or every NG-th
         const bool single = NG == 1 || u.count <= kSingle;
-        const int owner = single ? ord % NG : 0;
+        const int owner = single ? ord % NG : -1;
         for (int i = single ? (grp == owner ? 0 : u.count) : (grp + NG - done % NG) % NG; i < u.count; i += single ? 1 : NG) {
             const int n = done + i, st = n % SLOTS, turn = n / SLOTS;
             // the turn before is over (it may be another group's), so the parity is this turn's
@@ -664,48 +670,6 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
             for (int o = XOR0; o < XOR1; o <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
         }
 
-        // ---- the token groups joined, half of them into the other half, down to group 0 ----
-        if (NG > 1 && !single) {
-            if (!meet()) return;  // the last join's reads are done
-#pragma unroll
-            for (int half = NG / 2; half >= 1; half >>= 1) {
-                // a group writes where it was the last to read: region (reader) + NG / 2 - half
-                const int region = ((grp % half) + NG / 2 - half) * Gm::READERS + warp % Gm::READERS;
-                float4* at = jbuf + region * ND * 32 + lane;
-                float* jr = jm + region * 32;
-                if (grp >= half && grp < 2 * half) {
-#pragma unroll
-                    for (int x = 0; x < ND; ++x) at[x * 32] = make_float4(O[x][0], O[x][1], O[x][2], O[x][3]);
-                    if (T8 ? g == 0 : j == 0) {
-                        jr[ra & 15] = m[0];
-                        jr[rb & 15] = m[1];
-                        jr[16 + (ra & 15)] = l[0];
-                        jr[16 + (rb & 15)] = l[1];
-                    }
-                }
-                if (!meet()) return;
-                if (grp < half) {
-                    const float om0 = jr[ra & 15], om1 = jr[rb & 15];
-                    const float n0 = fmaxf(m[0], om0), n1 = fmaxf(m[1], om1);
-                    const float z0 = n0 == -INFINITY ? 0.0f : n0, z1 = n1 == -INFINITY ? 0.0f : n1;
-                    const float a0 = exp2_fast(m[0] - z0), a1 = exp2_fast(m[1] - z1);
-                    const float b0 = exp2_fast(om0 - z0), b1 = exp2_fast(om1 - z1);
-                    l[0] = l[0] * a0 + jr[16 + (ra & 15)] * b0;
-                    l[1] = l[1] * a1 + jr[16 + (rb & 15)] * b1;
-                    m[0] = n0;
-                    m[1] = n1;
-#pragma unroll
-                    for (int x = 0; x < ND; ++x) {
-                        const float4 o = at[x * 32];
-                        const float other[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) O[x][e] = O[x][e] * (second(e) ? a1 : a0) + other[e] * (second(e) ? b1 : b0);
-                    }
-                }
-            }
-        }
-
-        // ---- the owner's warps write the result, or the piece of it (fp32, unnormalised) ----
         const bool split = u.c0 != u.c1;
         const int rows = min(BM, u.n * G - u.rt * BM);
         if (split) {
@@ -714,10 +678,101 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
             if (which) split_last = true; else split_first = true;
             if (warp == 0 && lane == 0) pieces[NQ + which] = u;
         }
+        // where a piece goes (fp32, unnormalised)
+        float* mine = p.partial + (size_t)(blockIdx.x * 2 + ((int)blockIdx.x == u.c0)) * PSTRIDE;
+
+        // ---- the token groups joined: each leaves its output in shared memory, every thread sums
+        // four columns of a row over the groups and writes them (by a tree down to one group, whose
+        // warps then wrote alone, each unit cost 5000 to 8000 cycles more: JOIN_FIG) ----
+        if (NG > 1 && !single) {
+            constexpr int RND = Gm::RND, COLS = Gm::COLS, WCOLS = Gm::WCOLS, JPITCH = Gm::JPITCH, NT = kComputeWarps * 32;
+            constexpr int ITEMS = (BM * COLS / 4 + NT - 1) / NT;  // of a thread and round
+            auto column = [&](int round, int c) { return c / WCOLS * (D / CS) + round * WCOLS + c % WCOLS; };
+            uint2 z[Gm::ROUNDS][ITEMS];  // the gates, on their way meanwhile
+#pragma unroll
+            for (int y = 0; y < ITEMS; ++y) {
+                const int k = tid + y * NT, r = k / (COLS / 4), rr = u.rt * BM + r, t = rr / G;
+#pragma unroll
+                for (int round = 0; round < Gm::ROUNDS; ++round)
+                    z[round][y] = !split && p.gate.ptr && r < rows ? gate_of4(p, (size_t)u.first + t, u.h * G + rr - t * G, column(round, k % (COLS / 4) * 4))
+                                                                   : make_uint2(0, 0);
+            }
+            if (joins > 0 && !wait(rbar, (joins - 1) & 1)) return;  // the last join's reads are done
+            float* part = jbuf + grp * BM * JPITCH + cs * WCOLS;
+            if (cs == 0 && (T8 ? g == 0 : j == 0)) {
+                float* stat = jm + grp * 2 * BM;
+                stat[ra] = m[0];
+                stat[rb] = m[1];
+                stat[BM + ra] = l[0];
+                stat[BM + rb] = l[1];
+            }
+#pragma unroll
+            for (int round = 0; round < Gm::ROUNDS; ++round) {
+                if (round > 0 && !meet()) return;
+#pragma unroll
+                for (int x = 0; x < RND; ++x) {
+                    const float(&o)[4] = O[round * RND + x];
+                    if (T8 && !FP8) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) part[(ra + (e & 1)) * JPITCH + x * 16 + g + 8 * (e >> 1)] = o[e];
+                    } else if (T8) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            *reinterpret_cast<float2*>(part + (ra + e) * JPITCH + x * 16 + 2 * g) = make_float2(o[e], o[2 + e]);
+                    } else if (!FP8) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            *reinterpret_cast<float2*>(part + (e ? rb : ra) * JPITCH + x * 8 + 2 * j) = make_float2(o[2 * e], o[2 * e + 1]);
+                    } else if (x % 2 == 0) {  // tile x has the even columns, tile x + 1 the odd ones
+                        const float(&o1)[4] = O[round * RND + x + 1 - 2 * (x & 1)];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            *reinterpret_cast<float4*>(part + (e ? rb : ra) * JPITCH + x * 8 + 4 * j) = make_float4(o[2 * e], o1[2 * e], o[2 * e + 1], o1[2 * e + 1]);
+                    }
+                }
+                if (!meet()) return;
+#pragma unroll
+                for (int y = 0; y < ITEMS; ++y) {
+                    const int k = tid + y * NT, r = k / (COLS / 4), c = k % (COLS / 4) * 4, rr = u.rt * BM + r, t = rr / G;
+                    if (r >= rows) continue;
+                    float top = jm[r], w[NG], tot = 0.0f;
+#pragma unroll
+                    for (int i = 1; i < NG; ++i) top = fmaxf(top, jm[i * 2 * BM + r]);
+                    const float ref = top == -INFINITY ? 0.0f : top;
+                    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                    for (int i = 0; i < NG; ++i) {
+                        w[i] = exp2_fast(jm[i * 2 * BM + r] - ref);
+                        tot = fmaf(w[i], jm[i * 2 * BM + BM + r], tot);
+                        const float4 o = *reinterpret_cast<const float4*>(jbuf + (i * BM + r) * JPITCH + c);
+                        sum.x = fmaf(w[i], o.x, sum.x);
+                        sum.y = fmaf(w[i], o.y, sum.y);
+                        sum.z = fmaf(w[i], o.z, sum.z);
+                        sum.w = fmaf(w[i], o.w, sum.w);
+                    }
+                    const int head = u.h * G + rr - t * G;
+                    const size_t row = (size_t)u.first + t;
+                    if (split) *reinterpret_cast<float4*>(mine + r * D + column(round, c)) = sum;
+                    else write_out4(p, row, head, D, column(round, c), sum, p.sh.v_scale / tot, z[round][y]);
+                    if (round == 0 && c == 0) {
+                        if (split) {
+                            mine[BM * D + r] = top;
+                            mine[BM * D + BM + r] = tot;
+                        } else if (p.lse) {
+                            p.lse[row * p.sh.Hq + head] = (top + log2f(tot)) * kLn2;
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(rbar);
+            ++joins;
+        }
+
+        // ---- or the one group that has a short piece, or all of a unit, writes the result or the piece ----
         if (T8 && grp == owner) {
             // 32 columns at a time through this warp's part of shared memory, rows by rows: a lane holds
             // columns of two rows, but eight lanes write a row together
-            float* mine = p.partial + (size_t)(blockIdx.x * 2 + ((int)blockIdx.x == u.c0)) * PSTRIDE;
             float* mem = obuf + warp * (8 * Gm::OUTP);
             const float inv0 = p.sh.v_scale / l[0], inv1 = p.sh.v_scale / l[1];
             uint2 z[D / 32][2];
@@ -774,7 +829,6 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
             const int a = wm * 16 + g, r0 = u.rt * BM + a;
             const bool in0 = a < rows, in1 = a + 8 < rows;
             if (split) {
-                float* mine = p.partial + (size_t)(blockIdx.x * 2 + ((int)blockIdx.x == u.c0)) * PSTRIDE;
 #pragma unroll
                 for (int x = 0; x < ND; x += 2) {
                     const int col = cs * (ND * 8) + x * 8;
@@ -858,7 +912,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
     cudaError_t e = device_sms(&dev, &sms);
     if (e != cudaSuccess) return e;
     const size_t smem = Gm::SLOTS * (size_t)Gm::SLOTB + Gm::NQ * (size_t)Gm::QB + Gm::JOINB + Gm::OUTB + Gm::FIXED + ((size_t)a.B + 1) * 4;
-    static_assert(4 * 32 * 4 + Gm::NQ * Gm::BM * 4 + (Gm::NQ + 3) * (int)sizeof(Piece) + (Gm::SLOTS + Gm::NQ + 1) * 8 +
+    static_assert(Gm::NG * 2 * Gm::BM * 4 + Gm::NQ * Gm::BM * 4 + (Gm::NQ + 3) * (int)sizeof(Piece) + (Gm::SLOTS + Gm::NQ + 2) * 8 +
                       (Gm::SLOTS + Gm::NQ + 16) * 4 <= Gm::FIXED, "small data");
     static std::once_flag once[kMaxDevices];
     static cudaError_t set[kMaxDevices];
