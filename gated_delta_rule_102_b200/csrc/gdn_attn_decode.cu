@@ -48,8 +48,10 @@ constexpr int kLaunchRegs = 168;
 // us, with 12 for the longer ones 360; a mix of many short ones takes 80 with 12 for all, 62 with
 // 6 for the short ones.
 constexpr int kShortCost = 6, kUnitCost = 12;
-constexpr int kSingle = 4;    // a piece of so many slots or fewer is one token group's alone (1: 79 us instead of 68 at 16 to 300 tokens)
-constexpr int kMinShare = 8;  // places of a CTA at least: fewer CTAs, and joins, for little work
+// A piece of so many slots or fewer is one token group's alone (4: one sequence of 509 tokens takes
+// 14.5 us, 2: 12.6), and places of a CTA at least: fewer CTAs, and pieces to join, for little work
+// (8: 12.6 us, 4: 11.7, 2: 15.8).
+constexpr int kSingle = 2, kMinShare = 4;
 
 // Geometry: D head size, WM row groups of 16 query rows (0: eight rows).
 template <int D, bool FP8, int WM>
