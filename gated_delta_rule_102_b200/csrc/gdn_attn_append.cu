@@ -13,7 +13,10 @@
 // 64 bits and in turns (a 32-bit product is off by a thousandth of a radian at position 10^4
 // already), only its fraction goes to the 32-bit sine and cosine.
 // Bound by HBM at many rows, where instructions come close (about 200 a warp and row), and by
-// the latency of the dependent lookups at few.
+// the latency of the dependent lookups at few. Measured: 256 sequences of 16 rows, 16 query and 2
+// key/value heads of 256, bf16: 18.2 us for 84 MB (4.6 TB/s); 200 sequences of up to 16 rows, 32
+// and 8 heads of 128 to e4m3: 18.1 us (380 instructions a warp and row, of which the divisions by
+// the scale are a quarter); one row 3.1 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -12,9 +12,13 @@
 // TMEM. O is rescaled only when a row's maximum has grown by more than 2^8 since the last
 // time (P and the sums stay within range until then, and the quotient is the same).
 // Warps: four of softmax, one issues the products, three load keys, values and queries by TMA.
+// Units of several CTAs leave fp32 parts that a second launch joins over the whole GPU.
 //
 // Bound: a tile of 64 tokens at d = 256 is 64 KB of HBM, about 2700 cycles of an SM's share;
-// its products take about 1000 and the softmax of 128 rows about 1500.
+// its products take about 1000 and the softmax of 128 rows about 1900. Measured at 32 sequences of
+// 1000 to 8000 tokens, 128 rows (234 MB): 77 us, 3.0 TB/s: 3300 cycles a tile while it runs, the
+// rest the way to the first tile, the parts written (128 KB each) and the join. At d = 128 and 64
+// the softmax is what a tile takes.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -345,7 +345,7 @@ size_t gdn_decode_static_scratch_bytes(void);
  *   layer. page_table [table_rows][max_pages] int32 and seq_lens [table_rows] int32 are
  *   shared by all layers and indexed by SLOT like the GDN pools: the token at position
  *   p of slot s is row p % page_size of page page_table[s][p / page_size]. Entries that
- *   hold no page are -1. seq_lens[s] is the number of tokens stored BEFORE the step:
+ *   hold no page are -1, behind those that hold one. seq_lens[s] is the number of tokens stored BEFORE the step:
  *   gdn_qk_rope_append writes positions seq_lens[s] .. and gdn_attn_decode reads them
  *   too, and neither changes seq_lens, so every layer of the step sees the same lengths;
  *   the caller advances them once per step (by the accepted count after a speculative
@@ -360,7 +360,8 @@ size_t gdn_decode_static_scratch_bytes(void);
  *   flagged GDN_DEVICE_ERR_SLOT_RANGE, one whose length is negative or does not fit
  *   max_pages * page_size positions is skipped and flagged GDN_DEVICE_ERR_SEQLEN.
  *   A page number outside [0, num_pages) is flagged GDN_DEVICE_ERR_PAGE and neither
- *   read nor written. Slots of one call are distinct.
+ *   read nor written. Slots of one gdn_qk_rope_append call are distinct (two sequences
+ *   would write the same places); gdn_attn_decode may be given a slot twice.
  */
 enum { GDN_KV_BF16 = 0, GDN_KV_E4M3 = 1 };
 
@@ -393,7 +394,7 @@ typedef struct {
 
 /* Heads of token rows that need not be contiguous (slices of one projection): element
  * (row, head, i) at ptr[row * row_stride + head * head_stride + i]. Strides in elements,
- * multiples of 8, not negative; ptr 16-byte aligned. */
+ * multiples of 8, not negative (0: one row or head for all); ptr 16-byte aligned. */
 typedef struct {
     const uint16_t* ptr;
     int64_t row_stride;
@@ -420,8 +421,11 @@ gdn_status gdn_qk_rope_append(const gdn_attn_config* cfg, const gdn_kv_cache* ca
                               void* stream);
 
 /*
- * Attention of the new tokens over the cache (theirs included: append first), one
- * launch. Token t of a sequence at position p = seq_lens[slot] + t attends positions
+ * Attention of the new tokens over the cache (theirs included: append first): one
+ * launch, or two where a key/value head has many query rows T * Hq / Hkv (a bf16 cache with
+ * a page_size that is a multiple of 8, more than 16, 32 or 64 rows at d = 256, 128 or 64:
+ * products on the fifth-generation tensor cores and a second launch that joins the parts of
+ * split sequences). Token t of a sequence at position p = seq_lens[slot] + t attends positions
  * 0..p (the last `window` of them): x = sm_scale q.k (capped), P = softmax(x),
  *   out = (sum_j P_j v_j) * sigmoid(gate)                          (gate NULL: no gate)
  *   lse [rows][Hq] fp32 nullable: the natural logarithm of the sum of exp(x)
@@ -429,7 +433,9 @@ gdn_status gdn_qk_rope_append(const gdn_attn_config* cfg, const gdn_kv_cache* ca
  *   workspace of gdn_attn_decode_workspace_bytes(cfg, B, T) bytes, zeroed by the caller
  *            once before its first use; every call leaves its counters zeroed again.
  *            Calls that may run at the same time on the GPU need separate workspaces;
- *            one that is large enough serves any configuration.
+ *            one that is large enough serves any configuration. After a call that
+ *            raised GDN_DEVICE_ERR_TIMEOUT it has to be zeroed again, and the call's
+ *            outputs are unspecified.
  * Values of keys and values past a sequence's end are never used (they may be NaN), and
  * a non-finite value of a later drafted token does not reach the rows before it. Pages
  * that lie wholly before every row's window are not read. B <= 2048. Results do not
@@ -441,7 +447,8 @@ gdn_status gdn_attn_decode(const gdn_attn_config* cfg, const gdn_kv_cache* cache
                            const int32_t* slots, uint16_t* out, float* lse, int32_t* err_flag, void* workspace,
                            void* stream);
 
-/* Bytes of the workspace of gdn_attn_decode (0 for a configuration it refuses). */
+/* Bytes of the workspace of gdn_attn_decode for B sequences of up to T tokens (0 for a
+ * configuration it refuses). They depend on head_dim, kv_dtype, page_size, Hq/Hkv and T. */
 size_t gdn_attn_decode_workspace_bytes(const gdn_attn_config* cfg, int32_t B, int32_t T);
 
 /*
@@ -471,8 +478,8 @@ gdn_status gdn_rope_inv_freq_host(int32_t rotary_dim, double theta, double facto
  * reserve: gives slot i the pages for its next n_tokens[i] tokens (n_tokens NULL: T).
  * fork:    child dst[i] becomes a copy of parent src[i]: whole pages are shared, a
  *          partly filled last page is replaced by a new one, and copy_src[i], copy_dst[i]
- *          [n] say which page to copy where (-1, -1: none). The child's row must be
- *          empty. Reserved pages past the parent's length are not inherited.
+ *          [n] say which page to copy where (-1, -1: none; a skipped child's copy_dst
+ *          is -2). The child's row must be empty. Reserved pages past the parent's length are not inherited.
  * free:    releases every page of the rows and sets their lengths to 0 (a slot listed
  *          twice is released once).
  * compact: moves the pages in use to the front of the pool: copy_src, copy_dst
