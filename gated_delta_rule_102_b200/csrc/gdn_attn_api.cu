@@ -73,8 +73,9 @@ gdn_status check_cache(const gdn_kv_cache* c, const gdn::AttnShape& sh, gdn::Pag
     if (misaligned(c->k_pages, 16) || misaligned(c->v_pages, 16) || misaligned(c->page_table, 4) ||
         misaligned(c->seq_lens, 4))
         return GDN_ERR_MISALIGNED;
-    // token numbers (page * page_size + offset) and positions are 32-bit in the kernels
-    if ((long)c->num_pages * sh.page_size > 0x7fffffffL || (long)c->max_pages * sh.page_size > 0x7fffffffL)
+    // token numbers (page * page_size + offset) and positions are 32-bit in the kernels, which look up to
+    // a tile past a sequence's end
+    if ((long)c->num_pages * sh.page_size > 0x7fffffffL || (long)c->max_pages * sh.page_size > 0x7fff0000L)
         return GDN_ERR_UNSUPPORTED;
     *out = gdn::PagedCache{c->k_pages, c->v_pages, c->num_pages, c->page_table, c->table_rows, c->max_pages, c->seq_lens};
     return GDN_OK;

@@ -29,23 +29,27 @@ __device__ __forceinline__ void pdl_wait() {
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 }
 
-// Exclusive prefix sum over the block (kT threads); *total gets the sum.
+// Sums of counts stay at 2^31 - 1 once they get there: more than any pool has, in any order.
+__device__ __forceinline__ int add_sat(int a, int b) { return (int)min((unsigned)a + (unsigned)b, 0x7fffffffu); }
+
+// Exclusive prefix sum of counts over the block (kT threads); *total gets the sum.
 __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        if (lane >= o) x = add_sat(x, y);
     }
     if (lane == 31) warp_sums[warp] = x;
+    const int left = __shfl_up_sync(0xffffffffu, x, 1);
     __syncthreads();
     if (warp == 0) {
         int s = warp_sums[lane];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += y;
+            if (lane >= o) s = add_sat(s, y);
         }
         warp_sums[lane] = s;
     }
@@ -53,7 +57,7 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
     const int before = warp ? warp_sums[warp - 1] : 0;
     *total = warp_sums[kWarps - 1];
     __syncthreads();
-    return before + x - v;
+    return add_sat(before, lane ? left : 0);
 }
 
 // Calls take(rank, page) for the lowest `want` pages whose counter is 0, in any order of
@@ -125,10 +129,10 @@ __global__ void __launch_bounds__(kT) pages_reserve_kernel(const PageArgs p) {
         int sum;
         const int before = block_scan(need, warp_sums, &sum);
         if (i < p.n) {
-            prefix[i] = total + before;
+            prefix[i] = add_sat(total, before);
             start[i] = from;
         }
-        total += sum;
+        total = add_sat(total, sum);
     }
     if (threadIdx.x == 0) prefix[p.n] = total;
     __syncthreads();
@@ -202,8 +206,8 @@ __global__ void __launch_bounds__(kT) pages_fork_kernel(const PageArgs p, const 
         }
         int sum;
         const int before = block_scan(need, warp_sums, &sum);
-        if (i < p.n) prefix[i] = total + before;
-        total += sum;
+        if (i < p.n) prefix[i] = add_sat(total, before);
+        total = add_sat(total, sum);
     }
     if (threadIdx.x == 0) prefix[p.n] = total;
     __syncthreads();

@@ -194,3 +194,10 @@ def test_binding_refuses_cpu_tensors_and_foreign_functions():
         gdn.CallPlan(gdn.gdn_decode_step, 1)
     with pytest.raises(TypeError):
         gdn.GdnAttnConfig.make(16, 2, 256, 64, kv_dtype=torch.float16)
+
+
+def test_positions_leave_room_for_a_tile(L):
+    """A length near 2^31 would send a tile's end past it."""
+    edge = (0x7fff0000 // 64)
+    for call in (append, attn):
+        assert call(L, kv=cache(max_pages=edge + 1)) == UNS

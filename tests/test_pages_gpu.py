@@ -202,3 +202,17 @@ def test_forked_and_compacted_caches_hold_the_same_tokens():
     for s in text:
         if s not in (0, 3):
             assert torch.equal(read(s), text[s]), s
+
+
+def test_reserve_more_than_can_be_counted():
+    """Wishes whose sum passes 2^31 pages: the first sequences get theirs, the call is flagged."""
+    n, width = 2048, (1 << 20) + 8
+    table = torch.full((n, width), -1, dtype=torch.int32, device="cuda")
+    lens, refs = torch.zeros(n, dtype=torch.int32, device="cuda"), torch.zeros(100, dtype=torch.int32, device="cuda")
+    counts = torch.full((n,), width, dtype=torch.int32, device="cuda")
+    counts[0] = 3
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gdn.gdn_pages_reserve(1, torch.arange(n, dtype=torch.int32, device="cuda"), counts, table, lens, refs, err)
+    assert int(err) == gdn.GDN_DEVICE_ERR_PAGE
+    assert table[0, :4].tolist() == [0, 1, 2, -1] and refs[:4].tolist() == [1, 1, 1, 0] and int(refs.sum()) == 3
+    assert int(table[1:, :128].max()) == -1
