@@ -15,8 +15,8 @@
 // Bound by HBM at many rows, where instructions come close (about 200 a warp and row), and by
 // the latency of the dependent lookups at few. Measured: 256 sequences of 16 rows, 16 query and 2
 // key/value heads of 256, bf16: 18.2 us for 84 MB (4.6 TB/s); 200 sequences of up to 16 rows, 32
-// and 8 heads of 128 to e4m3: 18.1 us (380 instructions a warp and row, of which the divisions by
-// the scale are a quarter); one row 3.1 us.
+// and 8 heads of 128 to e4m3: 16.8 us (more than 300 instructions a warp and row, and CTAs of
+// unequal rows); one row 3.1 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -135,17 +135,43 @@ __device__ __forceinline__ void rotate_head(float (&x)[2][8], int sub, int R, Pa
     }
 }
 
+// A division by the cache's scale whose result is rounded to e4m3. A power of two: the product with
+// its inverse, exact (results so small that they are not are zeros). Else the product, off by at
+// most 2^-23 of itself: where the values 2^-21 to both sides of it round to the same, so does the
+// quotient, and only the rest is divided (a division an element took 18.1 us for 200 sequences of up
+// to 16 rows, so 16.8).
+struct Divisor {
+    float scale, inverse;
+    bool exact, near;
+    __device__ __forceinline__ explicit Divisor(float s) : scale(s), inverse(1.0f / s) {
+        const uint32_t bits = __float_as_uint(s), e = bits >> 23;
+        near = e >= 64 && e <= 190;  // the inverse is a normal number with room to either side
+        exact = near && (bits & 0x7fffffu) == 0;
+    }
+};
 // A lane's sixteen elements divided by the scale, as e4m3 (nowhere: a null pointer).
 template <int D>
-__device__ __forceinline__ void store_e4m3(const float (&x)[2][8], float scale, unsigned char* to) {
+__device__ __forceinline__ void store_e4m3(const float (&x)[2][8], const Divisor& by, unsigned char* to) {
     if (!to) return;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        float y[8];
+        uint32_t z[4];
+        bool sure = by.near;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) y[u] = __fdiv_rn(x[i][u], scale);
-        *reinterpret_cast<uint2*>(to + i * (D / 2)) =
-            make_uint2(e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16), e4m3x2(y[4], y[5]) | (e4m3x2(y[6], y[7]) << 16));
+        for (int u = 0; u < 8; u += 2) {
+            const float a = x[i][u] * by.inverse, b = x[i][u + 1] * by.inverse;
+            z[u / 2] = e4m3x2(a, b);
+            if (!by.exact) {
+                constexpr float kLess = 1.0f - 0x1p-21f, kMore = 1.0f + 0x1p-21f;
+                z[u / 2] = e4m3x2(a * kLess, b * kLess);
+                sure = sure && z[u / 2] == e4m3x2(a * kMore, b * kMore);
+            }
+        }
+        if (!sure) {
+#pragma unroll
+            for (int u = 0; u < 8; u += 2) z[u / 2] = e4m3x2(__fdiv_rn(x[i][u], by.scale), __fdiv_rn(x[i][u + 1], by.scale));
+        }
+        *reinterpret_cast<uint2*>(to + i * (D / 2)) = make_uint2(z[0] | (z[1] << 16), z[2] | (z[3] << 16));
     }
 }
 
@@ -237,7 +263,7 @@ __global__ void __launch_bounds__(kMostThreads, 2) qk_rope_append_kernel(const A
     unsigned char* to = is_q ? reinterpret_cast<unsigned char*>(p.q_out + (row0 * Hq + head) * D + sub * 8)
                              : static_cast<unsigned char*>(is_v ? p.c.v : p.c.k) + ((size_t)head * D + sub * 8) * ESZ;
     const long to_step = is_q ? (long)Hq * D * 2 : (long)Hkv * D * ESZ;
-    const float scale = is_v ? p.sh.v_scale : p.sh.k_scale;
+    const Divisor by(is_v ? p.sh.v_scale : p.sh.k_scale);
     __syncthreads();
 
     for (int t = 0; t < rows; ++t) {
@@ -273,7 +299,7 @@ __global__ void __launch_bounds__(kMostThreads, 2) qk_rope_append_kernel(const A
                     unpack8(w[0], x[0]);
                     unpack8(w[1], x[1]);
                 }
-                store_e4m3<D>(x, scale, active && token[t] >= 0 ? to + token[t] * to_step : nullptr);
+                store_e4m3<D>(x, by, active && token[t] >= 0 ? to + token[t] * to_step : nullptr);
             } else if (!is_v) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
@@ -283,7 +309,7 @@ __global__ void __launch_bounds__(kMostThreads, 2) qk_rope_append_kernel(const A
             float x[2][8];
             unpack8(w[0], x[0]);
             unpack8(w[1], x[1]);
-            store_e4m3<D>(x, scale, active && token[t] >= 0 ? to + token[t] * to_step : nullptr);
+            store_e4m3<D>(x, by, active && token[t] >= 0 ? to + token[t] * to_step : nullptr);
         }
         if (active && (is_q || (!FP8 && token[t] >= 0))) {
             uint4* at = reinterpret_cast<uint4*>(is_q ? to + t * to_step : to + token[t] * to_step);

@@ -226,3 +226,46 @@ def test_the_same_slot_twice_reads_the_same_cache():
     assert int(L.err) == 0
     # (their shares of the schedule differ, so the sums' order does)
     assert ((out[0].float() - out[2].float()).abs() <= 2.0 ** -6 * out[0].float().abs() + 2.0 ** -7).all()
+
+
+@pytest.mark.parametrize("d,G,T", [(128, 4, 1), (128, 4, 4), (256, 8, 16), (64, 16, 16)])
+@pytest.mark.parametrize("scale,softcap", [(-0.07, 0.0), (0.3, 0.0), (-0.2, 15.0)])
+def test_score_factors_and_other_strides(d, G, T, scale, softcap):
+    """A factor of its own, also a negative one; queries with heads outermost, one gate for all tokens."""
+    L = Layer([0, 63, 500], [T] * 3, T, 2 * G, 2, d, 16, sm_scale=scale, softcap=softcap)
+    kp, vp = L.pool(1.5), L.pool()
+    q = L.randn(2 * G, 3, T, d).permute(1, 2, 0, 3)
+    q = q.as_strided(q.shape, (T * d, d, 3 * T * d, 1))
+    gate = L.randn(1, 1, 2 * G, d).expand(3, T, 2 * G, d)
+    out = torch.empty(3, T, 2 * G, d, dtype=BF16, device=DEV)
+    gdn.gdn_attn_decode(L.cfg, q, kp, vp, L.table, L.lens, L.slots, out, gdn.attn_decode_workspace(L.cfg, 3, T, DEV), gate=gate,
+                        err_flag=L.err)
+    assert int(L.err) == 0
+    for b in range(3):
+        n = L.past[b] + T
+        kk, vv = L.tokens(kp, b, n), L.tokens(vp, b, n)
+        want, _, mass, _ = attention(q[b], kk, vv, L.past[b], scale, softcap, 0, gate[b])
+        big = attention(q[b], kk, vv, L.past[b], abs(scale), softcap, 0)[3]
+        eps_x = 2 * d * 2.0 ** -24 * big + softcap * 2.0 ** -21
+        tol = (2 * eps_x + 2.0 ** -20 + 2.0 ** -8)[..., None] * mass + 2.0 ** -8 * want.abs()
+        assert ((out[b].double() - want).abs() <= tol).all(), b
+
+
+@pytest.mark.parametrize("scale", [1e-30, 2.0 ** -80, 2.0 ** -40, 0.3, 1.0, 3.0, 1e25, 2.0 ** 100])
+def test_append_divides_by_any_scale(scale):
+    """Stored values are the quotients' roundings to the last bit, ties and the ends of the range among them."""
+    d, Hkv, B = 128, 8, 64
+    L = Layer([0] * B, [1] * B, 1, Hkv, Hkv, d, 1, E4M3)
+    cfg = gdn.GdnAttnConfig.make(Hkv, Hkv, d, 1, kv_dtype=E4M3, k_scale=1.0, v_scale=scale)
+    scale = cfg.v_scale  # (as 32 bits)
+    q = L.randn(B, 1, Hkv, d)
+    # quotients between e4m3's smallest and largest values, on and around its ties
+    v = (torch.randn(B, 1, Hkv, d, generator=L.gpu, device=DEV).double() * 2.0 ** torch.randint(-11, 10, (B, 1, Hkv, d), generator=L.gpu, device=DEV)
+         * scale).clamp(-3e38, 3e38).to(BF16)
+    v[0, 0, 0, :6] = torch.tensor([0.0, -0.0, float("inf"), float("-inf"), 3e38, 1e-38]).to(BF16)
+    kp, vp = L.pool(), L.pool()
+    gdn.gdn_qk_rope_append(cfg, q, q, v, None, None, None, kp, vp, L.table, L.lens, L.slots, torch.empty_like(q), err_flag=L.err)
+    assert int(L.err) == 0
+    want = (v.float() / torch.full_like(v, scale, dtype=F32)).clamp(-448, 448).to(E4M3)
+    page = L.table[L.slots.long(), 0].long()
+    assert torch.equal(view(vp, E4M3)[page, 0], view(want, E4M3)[:, 0])
