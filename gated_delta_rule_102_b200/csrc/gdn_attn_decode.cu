@@ -107,7 +107,8 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
     Piece* pieces = reinterpret_cast<Piece*>(qexp + NQ * BM);     // [NQ], then the share's first and last split ones
     uint64_t* full = reinterpret_cast<uint64_t*>(pieces + NQ + 2 + ((NQ + 2) & 1));  // [SLOTS]
     uint64_t* qfull = full + SLOTS;                               // [NQ]
-    uint64_t* cbar = qfull + NQ;                                  // the computing warps' barrier
+    uint64_t* qraw = qfull + NQ;                                  // [NQ] (e4m3) the queries as they came
+    uint64_t* cbar = qraw + NQ;                                   // the computing warps' barrier
     // Releases are counted, not phased: a warp comes back to a place only every few turns, and
     // a barrier's phase parity cannot tell a turn from the one two before it.
     uint64_t* rbar = cbar + 1;                                    // their reads of the last join
@@ -125,7 +126,8 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
             freed[i] = 0;
         }
         for (int i = 0; i < NQ; ++i) {
-            mbar_init(qfull + i, FP8 ? 32 : 1);
+            mbar_init(qfull + i, 1);
+            mbar_init(qraw + i, 1);
             qfreed[i] = 0;
         }
         mbar_init(cbar, kComputeWarps);
@@ -172,76 +174,83 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
 
     if (warp == kComputeWarps + kLoadWarps) {
         // ================= queries =================
+        // As many units' queries are on their way as there is room for; those of an e4m3 cache are
+        // converted when they have come (one unit at a time, load and conversion, 96 sequences of up
+        // to 16000 tokens took 62 us, so 60: its CTAs of many short units waited for queries).
         bool more_units = true;
-        int sent = 0;
-        for (int ord = 0; more_units; ++ord) {
-            const Seq c = at.s;
-            const int rt = at.unit / Hkv, h = at.unit - rt * Hkv, place = at.place, from = at.tile;
-            more_units = at.next_unit();  // before this one is described: it may be the last
-            at.tile = 0;
-            // the unit's queries: row r is token r / G, query head h * G + r % G; rows past the last
-            // are left as they are (a row's products touch no other row)
-            const int qs = ord % NQ, rows = min(BM, c.n * G - rt * BM);
-            const int inv_g = 65536 / G + 1;  // r / G = r * inv_g >> 16 for r < 320, G <= 16
-            if (!wait_count(qfreed + qs, ord / NQ * kComputeWarps)) break;
-            sent = ord + 1;
+        int sent = 0, converted = 0;
+        const int inv_g = 65536 / G + 1;  // r / G = r * inv_g >> 16 for r < 320, G <= 16
+        while (true) {
+            const bool to_convert = FP8 && converted < sent;
+            if (more_units && (!to_convert || __shfl_sync(0xffffffffu, load_acquire(qfreed + sent % NQ), 0) >= sent / NQ * kComputeWarps)) {
+                const Seq c = at.s;
+                const int rt = at.unit / Hkv, h = at.unit - rt * Hkv, place = at.place, from = at.tile;
+                more_units = at.next_unit();  // before this one is described: it may be the last
+                at.tile = 0;
+                // the unit's queries: row r is token r / G, query head h * G + r % G; rows past the last
+                // are left as they are (a row's products touch no other row)
+                const int qs = sent % NQ, rows = min(BM, c.n * G - rt * BM);
+                if (!wait_count(qfreed + qs, sent / NQ * kComputeWarps)) break;
+                ++sent;
+                unsigned char* q = qbuf + qs * QB;
+                uint64_t* bar = (FP8 ? qraw : qfull) + qs;
+                if (lane == 0) {
+                    pieces[qs] = Piece{c.n, c.first, c.past, c.lo, c.base, h, rt, from, min(c.tiles - from, at.hi - place - from),
+                                       !more_units, at.cta_of(place), at.cta_of(place + c.tiles - 1)};
+                    mbar_arrive_expect_tx(bar, rows * D * 2);
+                }
+                __syncwarp();
+                for (int r = lane; r < rows; r += 32) {
+                    const int rr = rt * BM + r, t = (rr * inv_g) >> 16;
+                    tma_load_1d(q + r * QP, p.q.ptr + (size_t)(c.first + t) * p.q.row + (size_t)(h * G + rr - t * G) * p.q.head, D * 2, bar);
+                }
+                if (p.gate.ptr) {  // the gates' lines into L2: they are read when the unit ends
+                    for (int i = lane; i < rows * (D / 64); i += 32) {
+                        const int r = i / (D / 64), rr = rt * BM + r, t = (rr * inv_g) >> 16;
+                        const uint16_t* line = p.gate.ptr + (size_t)(c.first + t) * p.gate.row + (size_t)(h * G + rr - t * G) * p.gate.head;
+                        asm volatile("prefetch.global.L2 [%0];\n" ::"l"(line + i % (D / 64) * 64));
+                    }
+                }
+                continue;
+            }
+            if (!to_convert) break;
+            // e4m3 keys become fp16, so the queries do too: a power of two per row brings its
+            // largest element to 2^14 .. 2^15, exact for every element above 2^-38 of that
+            constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes a row, rows at a time
+            const int qs = converted % NQ;
+            if (!wait(qraw + qs, (converted / NQ) & 1)) break;
+            const int rows = min(BM, pieces[qs].n * G - pieces[qs].rt * BM);
             unsigned char* q = qbuf + qs * QB;
-            if (lane == 0) {
-                pieces[qs] = Piece{c.n, c.first, c.past, c.lo, c.base, h, rt, from, min(c.tiles - from, at.hi - place - from),
-                                   !more_units, at.cta_of(place), at.cta_of(place + c.tiles - 1)};
-                if (!FP8) mbar_arrive_expect_tx(qfull + qs, rows * D * 2);
+#pragma unroll 1  // (unrolled by four, 256 short sequences take 69 us instead of 62: the instruction caches)
+            for (int r0 = 0; r0 < rows; r0 += RPW) {
+                const int r = r0 + lane / LPR, ch = lane % LPR;
+                uint4* word = reinterpret_cast<uint4*>(q + r * QP + ch * 16);
+                const uint4 in = r < rows ? *word : make_uint4(0, 0, 0, 0);
+                const uint32_t v[4] = {in.x, in.y, in.z, in.w};
+                uint32_t top = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top = max(top, max(v[k] & 0x7fffu, (v[k] >> 16) & 0x7fffu));
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const int e = top == 0 || top >= 0x7f80u ? 0 : max((int)(top >> 7), 1) - 127 - 14;
+                // 2^-e: e is at most 113, and at least -140, where the exponent field ends
+                const float up = __uint_as_float((uint32_t)(127 - max(e, -127)) << 23);
+                uint32_t z[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) z[k] = pack2<true>(__uint_as_float(v[k] << 16) * up, __uint_as_float(v[k] & 0xffff0000u) * up);
+                if (r < rows) {
+                    *word = make_uint4(z[0], z[1], z[2], z[3]);
+                    if (ch == 0) qexp[qs * BM + r] = 1.0f / up;
+                }
             }
+            fence_proxy_async_smem();  // before queries come to this place again
             __syncwarp();
-            auto row_of = [&](int r) {
-                const int rr = rt * BM + r, t = (rr * inv_g) >> 16;
-                return p.q.ptr + (size_t)(c.first + t) * p.q.row + (size_t)(h * G + rr - t * G) * p.q.head;
-            };
-            if (!FP8) {
-                for (int r = lane; r < rows; r += 32) tma_load_1d(q + r * QP, row_of(r), D * 2, qfull + qs);
-            } else {
-                // e4m3 keys become fp16, so the queries do too: a power of two per row brings its
-                // largest element to 2^14 .. 2^15, exact for every element above 2^-38 of that
-                constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes a row, rows at a time
-                for (int r0 = 0; r0 < rows; r0 += 8 * RPW) {  // eight loads in flight
-                    uint4 in[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = r0 + i * RPW + lane / LPR;
-                        in[i] = r < rows ? __ldg(reinterpret_cast<const uint4*>(row_of(r)) + lane % LPR) : make_uint4(0, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = r0 + i * RPW + lane / LPR, ch = lane % LPR;
-                        if (r0 + i * RPW >= rows) break;  // the same for every lane
-                        const uint32_t v[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
-                        uint32_t top = 0;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) top = max(top, max(v[k] & 0x7fffu, (v[k] >> 16) & 0x7fffu));
-#pragma unroll
-                        for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        const int e = top == 0 || top >= 0x7f80u ? 0 : max((int)(top >> 7), 1) - 127 - 14;
-                        // 2^-e: e is at most 113, and at least -140, where the exponent field ends
-                        const float up = __uint_as_float((uint32_t)(127 - max(e, -127)) << 23);
-                        uint32_t z[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) z[k] = pack2<true>(__uint_as_float(v[k] << 16) * up, __uint_as_float(v[k] & 0xffff0000u) * up);
-                        *reinterpret_cast<uint4*>(q + r * QP + ch * 16) = make_uint4(z[0], z[1], z[2], z[3]);
-                        if (ch == 0) qexp[qs * BM + r] = 1.0f / up;
-                    }
-                }
-                mbar_arrive(qfull + qs);
-            }
-            if (p.gate.ptr) {  // the gates' lines into L2: they are read when the unit ends
-                for (int i = lane; i < rows * (D / 64); i += 32) {
-                    const int r = i / (D / 64), rr = rt * BM + r, t = (rr * inv_g) >> 16;
-                    const uint16_t* line = p.gate.ptr + (size_t)(c.first + t) * p.gate.row + (size_t)(h * G + rr - t * G) * p.gate.head;
-                    asm volatile("prefetch.global.L2 [%0];\n" ::"l"(line + i % (D / 64) * 64));
-                }
-            }
+            if (lane == 0) mbar_arrive(qfull + qs);
+            ++converted;
         }
         // after an abort: what is in flight lands before the block leaves
-        if (*stop != 0 && !FP8) {
-            for (int i = max(0, sent - NQ); i < sent; ++i) mbar_wait_bounded(qfull + i % NQ, (i / NQ) & 1);
+        if (*stop != 0) {
+            for (int i = FP8 ? converted : max(0, sent - NQ); i < sent; ++i) mbar_wait_bounded((FP8 ? qraw : qfull) + i % NQ, (i / NQ) & 1);
         }
         return;
     }
@@ -920,7 +929,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
     cudaError_t e = device_sms(&dev, &sms);
     if (e != cudaSuccess) return e;
     const size_t smem = Gm::SLOTS * (size_t)Gm::SLOTB + Gm::NQ * (size_t)Gm::QB + Gm::JOINB + Gm::OUTB + Gm::FIXED + ((size_t)a.B + 1) * 4;
-    static_assert(Gm::NG * 2 * Gm::BM * 4 + Gm::NQ * Gm::BM * 4 + (Gm::NQ + 3) * (int)sizeof(Piece) + (Gm::SLOTS + Gm::NQ + 2) * 8 +
+    static_assert(Gm::NG * 2 * Gm::BM * 4 + Gm::NQ * Gm::BM * 4 + (Gm::NQ + 3) * (int)sizeof(Piece) + (Gm::SLOTS + 2 * Gm::NQ + 2) * 8 +
                       (Gm::SLOTS + Gm::NQ + 16) * 4 <= Gm::FIXED, "small data");
     static std::once_flag once[kMaxDevices];
     static cudaError_t set[kMaxDevices];
