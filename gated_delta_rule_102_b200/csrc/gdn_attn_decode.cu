@@ -9,7 +9,7 @@
 // cost is its number of token tiles. One CTA per SM takes an equal, contiguous share of
 // all token tiles of the launch (the schedule follows from the lengths, which are read on
 // the device: every CTA sums the tile counts of the batch). A unit that spans CTAs leaves
-// one partial result (running maximum, sum, unnormalised output, fp32) per CTA in the
+// one partial result (reference of its scores, sum, unnormalised output, fp32) per CTA in the
 // workspace, and the last CTA to finish joins them in CTA order: the result does not
 // depend on which one that is. A CTA has at most two partial pieces, one at each end of
 // its share, so the workspace does not grow with the lengths.
@@ -102,7 +102,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
     unsigned char* qbuf = ring + SLOTS * Gm::SLOTB;
     float* jbuf = reinterpret_cast<float*>(qbuf + NQ * QB);       // [NG][BM][JPITCH] outputs to be joined
     float* obuf = reinterpret_cast<float*>(qbuf + NQ * QB + Gm::JOINB);  // (T8) [8 warps][8][OUTP]
-    float* jm = reinterpret_cast<float*>(qbuf + NQ * QB + Gm::JOINB + Gm::OUTB);  // [NG][2][BM] their maxima and sums
+    float* jm = reinterpret_cast<float*>(qbuf + NQ * QB + Gm::JOINB + Gm::OUTB);  // [NG][2][BM] their references and sums
     float* qexp = jm + NG * 2 * BM;                                   // [NQ][BM] (e4m3) power of two taken out of a query row
     Piece* pieces = reinterpret_cast<Piece*>(qexp + NQ * BM);     // [NQ], then the share's first and last split ones
     uint64_t* full = reinterpret_cast<uint64_t*>(pieces + NQ + 2 + ((NQ + 2) & 1));  // [SLOTS]
@@ -375,7 +375,8 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
         float O[ND][4];
 #pragma unroll
         for (int i = 0; i < ND; ++i) O[i][0] = O[i][1] = O[i][2] = O[i][3] = 0.0f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};  // rows ra, rb: maximum (log2 units), sum
+        // rows ra, rb: reference (log2 units: the maximum so far, or near it with an e4m3 cache), sum
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 
         // this group's slots: all of a short piece, in turn with the other groups, or every NG-th
         const bool single = NG == 1 || u.count <= kSingle;
@@ -499,7 +500,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                         for (int e = 0; e < 4; ++e) S[x][e] += S[o * NS + x][e];
                     }
                 }
-                float mx0 = m[0], mx1 = m[1];
+                float mx0 = FP8 ? -INFINITY : m[0], mx1 = FP8 ? -INFINITY : m[1];
                 if (capped) {
 #pragma unroll
                     for (int x = 0; x < NS; ++x) {
@@ -534,6 +535,10 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                 for (int o = XOR0; o < XOR1; o <<= 1) {
                     mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
                     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+                }
+                if (FP8) {
+                    mx0 = fmaxf(m[0], fp16_reference(mx0));
+                    mx1 = fmaxf(m[1], fp16_reference(mx1));
                 }
                 const float ref0 = mx0 == -INFINITY ? 0.0f : mx0, ref1 = mx1 == -INFINITY ? 0.0f : mx1;  // nothing seen yet
                 if (__any_sync(0xffffffffu, mx0 != m[0] || mx1 != m[1])) {
@@ -776,7 +781,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                             mine[BM * D + r] = top;
                             mine[BM * D + BM + r] = tot;
                         } else if (p.lse) {
-                            p.lse[row * p.sh.Hq + head] = (top + log2f(tot)) * kLn2;
+                            p.lse[row * p.sh.Hq + head] = log_sum(p, top, tot);
                         }
                     }
                 }
@@ -837,7 +842,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                         mine[BM * D + r] = m[e];
                         mine[BM * D + BM + r] = l[e];
                     } else if (p.lse) {
-                        p.lse[((size_t)u.first + t) * p.sh.Hq + u.h * G + rr - t * G] = (m[e] + log2f(l[e])) * kLn2;
+                        p.lse[((size_t)u.first + t) * p.sh.Hq + u.h * G + rr - t * G] = log_sum(p, m[e], l[e]);
                     }
                 }
             }
@@ -911,7 +916,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                             *reinterpret_cast<uint2*>(out + x * 16 + 4 * j) = make_uint2(pack2<false>(v0, v1), pack2<false>(v2, v3));
                         }
                     }
-                    if (p.lse && cs == 0 && j == 0) p.lse[at] = (m[e] + log2f(l[e])) * kLn2;
+                    if (p.lse && cs == 0 && j == 0) p.lse[at] = log_sum(p, m[e], l[e]);
                 }
             }
         }

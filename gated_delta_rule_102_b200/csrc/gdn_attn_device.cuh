@@ -289,6 +289,20 @@ struct Share {
     }
 };
 
+// With an e4m3 cache the probabilities are fp16, whose normal numbers end at 2^-14 and whose smallest
+// is 2^-24. So a row's reference lies kUp below its maximum: P goes up to 2^15, is rounded once to 11
+// bits down to 2^-29 of the row's largest, and vanishes below 2^-40 of it. (With the maximum itself the
+// same came at 2^-14 and 2^-25, which a flat tail of many tokens below a sink reaches.) Sums and outputs
+// carry the factor, and their quotient cancels it. A reference may be any number near the maximum as
+// long as one row uses one; beyond 2^22, where 32 bits cannot place it to a quarter, it is the maximum.
+constexpr float kUp = 15.0f;
+__device__ __forceinline__ float fp16_reference(float top) { return fabsf(top) < 0x1p22f ? top - kUp : top; }
+// The natural logarithm of a row's sum from its reference and the sum of exp2(x - reference). (The factor
+// goes first: the logarithm of a sum of 2^15 has four bits fewer behind the point.)
+__device__ __forceinline__ float log_sum(const AttnArgs& p, float ref, float sum) {
+    return p.sh.fp8 ? ((ref + kUp) + log2f(sum * 0x1p-15f)) * kLn2 : (ref + log2f(sum)) * kLn2;
+}
+
 // Four columns of an output row: their gates (read apart, so that many are in flight), and the
 // values normalised, gated and rounded once.
 __device__ __forceinline__ uint2 gate_of4(const AttnArgs& p, size_t row, int head, int col) {
@@ -416,7 +430,7 @@ __device__ __forceinline__ bool join_units(const AttnArgs& p, const Piece* share
                     const size_t row = (size_t)u.first + t;
                     const float* w = wt + r * WP;
                     write_out4(p, row, head, D, col, o[y], p.sh.v_scale / w[kJoinMost], z[y]);
-                    if (p.lse && col == 0) p.lse[row * p.sh.Hq + head] = (w[kJoinMost + 1] + log2f(w[kJoinMost])) * kLn2;
+                    if (p.lse && col == 0) p.lse[row * p.sh.Hq + head] = log_sum(p, w[kJoinMost + 1], w[kJoinMost]);
                 }
             }
             if (tid == 0) *counter = 0;
