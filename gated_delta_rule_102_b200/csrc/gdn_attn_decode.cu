@@ -775,13 +775,13 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                     const int head = u.h * G + rr - t * G;
                     const size_t row = (size_t)u.first + t;
                     if (split) *reinterpret_cast<float4*>(mine + r * D + column(round, c)) = sum;
-                    else write_out4(p, row, head, D, column(round, c), sum, p.sh.v_scale / tot, z[round][y]);
+                    else write_out4<FP8>(p, row, head, D, column(round, c), sum, 1.0f / tot, z[round][y]);
                     if (round == 0 && c == 0) {
                         if (split) {
                             mine[BM * D + r] = top;
                             mine[BM * D + BM + r] = tot;
                         } else if (p.lse) {
-                            p.lse[row * p.sh.Hq + head] = log_sum(p, top, tot);
+                            p.lse[row * p.sh.Hq + head] = log_sum<FP8>(top, tot);
                         }
                     }
                 }
@@ -796,7 +796,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
             // 32 columns at a time through this warp's part of shared memory, rows by rows: a lane holds
             // columns of two rows, but eight lanes write a row together
             float* mem = obuf + warp * (8 * Gm::OUTP);
-            const float inv0 = p.sh.v_scale / l[0], inv1 = p.sh.v_scale / l[1];
+            const float inv0 = 1.0f / l[0], inv1 = 1.0f / l[1];
             uint2 z[D / 32][2];
             float inv[2];
             int head[2];
@@ -830,7 +830,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                     const float4 o = *reinterpret_cast<const float4*>(mem + r * Gm::OUTP + (lane & 7) * 4);
                     if (r >= rows) continue;
                     if (split) *reinterpret_cast<float4*>(mine + r * D + col) = o;
-                    else write_out4(p, row[y], head[y], D, col, o, inv[y], z[c][y]);
+                    else write_out4<FP8>(p, row[y], head[y], D, col, o, inv[y], z[c][y]);
                 }
             }
             if (g == 0) {
@@ -842,7 +842,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                         mine[BM * D + r] = m[e];
                         mine[BM * D + BM + r] = l[e];
                     } else if (p.lse) {
-                        p.lse[((size_t)u.first + t) * p.sh.Hq + u.h * G + rr - t * G] = log_sum(p, m[e], l[e]);
+                        p.lse[((size_t)u.first + t) * p.sh.Hq + u.h * G + rr - t * G] = log_sum<FP8>(m[e], l[e]);
                     }
                 }
             }
@@ -882,7 +882,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                     const size_t row = (size_t)u.first + t, at = row * p.sh.Hq + head;
                     uint16_t* out = p.out + at * D + cs * (ND * 8);
                     const uint16_t* gate = p.gate.ptr + row * p.gate.row + (size_t)head * p.gate.head + cs * (ND * 8);
-                    const float inv = p.sh.v_scale / l[e];
+                    const float inv = 1.0f / l[e];
                     if (!FP8) {
                         uint32_t z[ND];
                         if (p.gate.ptr) {
@@ -906,7 +906,9 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                         }
 #pragma unroll
                         for (int x = 0; x < ND / 2; ++x) {
-                            float v0 = O[2 * x][2 * e] * inv, v1 = O[2 * x + 1][2 * e] * inv, v2 = O[2 * x][2 * e + 1] * inv, v3 = O[2 * x + 1][2 * e + 1] * inv;
+                            const float s = p.sh.v_scale;  // (by itself, as in write_out4)
+                            float v0 = O[2 * x][2 * e] * inv * s, v1 = O[2 * x + 1][2 * e] * inv * s;
+                            float v2 = O[2 * x][2 * e + 1] * inv * s, v3 = O[2 * x + 1][2 * e + 1] * inv * s;
                             if (p.gate.ptr) {
                                 v0 *= sigmoid_fast(__uint_as_float(z[x].x << 16));
                                 v1 *= sigmoid_fast(__uint_as_float(z[x].x & 0xffff0000u));
@@ -916,14 +918,14 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                             *reinterpret_cast<uint2*>(out + x * 16 + 4 * j) = make_uint2(pack2<false>(v0, v1), pack2<false>(v2, v3));
                         }
                     }
-                    if (p.lse && cs == 0 && j == 0) p.lse[at] = log_sum(p, m[e], l[e]);
+                    if (p.lse && cs == 0 && j == 0) p.lse[at] = log_sum<FP8>(m[e], l[e]);
                 }
             }
         }
     }
 
     static_assert(BM * (kJoinMost + 2) * 4 <= SLOTS * Gm::SLOTB, "weights");
-    join_units<D, BM, kComputeWarps * 32>(p, pieces + NQ, split_first, split_last, BM, reinterpret_cast<float*>(ring), misc + 12, meet);
+    join_units<D, FP8, BM, kComputeWarps * 32>(p, pieces + NQ, split_first, split_last, BM, reinterpret_cast<float*>(ring), misc + 12, meet);
 }
 
 template <int D, bool FP8, int WM>

@@ -299,8 +299,9 @@ constexpr float kUp = 15.0f;
 __device__ __forceinline__ float fp16_reference(float top) { return fabsf(top) < 0x1p22f ? top - kUp : top; }
 // The natural logarithm of a row's sum from its reference and the sum of exp2(x - reference). (The factor
 // goes first: the logarithm of a sum of 2^15 has four bits fewer behind the point.)
-__device__ __forceinline__ float log_sum(const AttnArgs& p, float ref, float sum) {
-    return p.sh.fp8 ? ((ref + kUp) + log2f(sum * 0x1p-15f)) * kLn2 : (ref + log2f(sum)) * kLn2;
+template <bool FP8>
+__device__ __forceinline__ float log_sum(float ref, float sum) {
+    return FP8 ? ((ref + kUp) + log2f(sum * 0x1p-15f)) * kLn2 : (ref + log2f(sum)) * kLn2;
 }
 
 // Four columns of an output row: their gates (read apart, so that many are in flight), and the
@@ -308,11 +309,18 @@ __device__ __forceinline__ float log_sum(const AttnArgs& p, float ref, float sum
 __device__ __forceinline__ uint2 gate_of4(const AttnArgs& p, size_t row, int head, int col) {
     return __ldg(reinterpret_cast<const uint2*>(p.gate.ptr + row * p.gate.row + (size_t)head * p.gate.head + col));
 }
+template <bool FP8>
 __device__ __forceinline__ void write_out4(const AttnArgs& p, size_t row, int head, int d, int col, float4 o, float inv, uint2 z) {
     o.x *= inv;
     o.y *= inv;
     o.z *= inv;
     o.w *= inv;
+    if (FP8) {  // the cache's scale by itself: a tiny one over the sum might not be a normal number
+        o.x *= p.sh.v_scale;
+        o.y *= p.sh.v_scale;
+        o.z *= p.sh.v_scale;
+        o.w *= p.sh.v_scale;
+    }
     if (p.gate.ptr) {
         o.x *= sigmoid_fast(__uint_as_float(z.x << 16));
         o.y *= sigmoid_fast(__uint_as_float(z.x & 0xffff0000u));
@@ -332,7 +340,7 @@ __device__ __forceinline__ void write_out4(const AttnArgs& p, size_t row, int he
 // All NT threads that meet() joins, after each has written its part of the pieces.
 // shared_pieces: the share's first and last split piece; wt: BM * (kJoinMost + 2) floats and
 // flag: one int of shared memory. row_tile: query rows of a unit (BM, or fewer).
-template <int D, int BM, int NT, typename Meet>
+template <int D, bool FP8, int BM, int NT, typename Meet>
 __device__ __forceinline__ bool join_units(const AttnArgs& p, const Piece* shared_pieces, bool split_first, bool split_last,
                                            int row_tile, float* wt, volatile int* flag, Meet meet) {
     constexpr int WP = kJoinMost + 2, PSTRIDE = BM * (D + 2);
@@ -429,8 +437,8 @@ __device__ __forceinline__ bool join_units(const AttnArgs& p, const Piece* share
                     const int rr = u.rt * row_tile + r, t = (rr * inv_g) >> 16, head = u.h * G + rr - t * G;
                     const size_t row = (size_t)u.first + t;
                     const float* w = wt + r * WP;
-                    write_out4(p, row, head, D, col, o[y], p.sh.v_scale / w[kJoinMost], z[y]);
-                    if (p.lse && col == 0) p.lse[row * p.sh.Hq + head] = log_sum(p, w[kJoinMost + 1], w[kJoinMost]);
+                    write_out4<FP8>(p, row, head, D, col, o[y], 1.0f / w[kJoinMost], z[y]);
+                    if (p.lse && col == 0) p.lse[row * p.sh.Hq + head] = log_sum<FP8>(w[kJoinMost + 1], w[kJoinMost]);
                 }
             }
             if (tid == 0) *counter = 0;

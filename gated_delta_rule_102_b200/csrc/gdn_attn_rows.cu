@@ -402,7 +402,7 @@ attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUt
                             *reinterpret_cast<float4*>(mine + r * D + c + q * 4) = v;
                         } else {
                             const int qr = u.rt * row_tile + r, qt = (qr * inv_g) >> 16;
-                            write_out4(p, (size_t)u.first + qt, u.h * G + qr - qt * G, D, c + q * 4, v, scale, z[e]);
+                            write_out4<false>(p, (size_t)u.first + qt, u.h * G + qr - qt * G, D, c + q * 4, v, scale, z[e]);
                         }
                     }
                 }
@@ -411,7 +411,7 @@ attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUt
                         mine[kRowTile * D + tid] = ref;
                         mine[kRowTile * D + kRowTile + tid] = sum;
                     } else if (p.lse) {
-                        p.lse[row * p.sh.Hq + head] = (ref + log2f(sum)) * kLn2;
+                        p.lse[row * p.sh.Hq + head] = log_sum<false>(ref, sum);
                     }
                 }
             }
@@ -533,8 +533,8 @@ __global__ void __launch_bounds__(kThreads) attn_rows_join_kernel(const __grid_c
         const int rr = u.rt * row_tile + base + r, t = (rr * inv_g) >> 16, head = u.h * G + rr - t * G;
         const size_t row = (size_t)u.first + t;
         const float* w = wt + r * WP;
-        write_out4(p, row, head, D, col, o[y], 1.0f / w[kAttnMaxCtas], z[y]);
-        if (p.lse && col == 0) p.lse[row * p.sh.Hq + head] = (w[kAttnMaxCtas + 1] + log2f(w[kAttnMaxCtas])) * kLn2;
+        write_out4<false>(p, row, head, D, col, o[y], 1.0f / w[kAttnMaxCtas], z[y]);
+        if (p.lse && col == 0) p.lse[row * p.sh.Hq + head] = log_sum<false>(w[kAttnMaxCtas + 1], w[kAttnMaxCtas]);
     }
 }
 
