@@ -336,8 +336,9 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
     constexpr int XOR0 = T8 ? 4 : 1, XOR1 = T8 ? 32 : 4;
     const bool capped = p.sh.softcap > 0.0f;
     const float qk_scale = p.sh.sm_scale * p.sh.k_scale;
-    const float to_log2 = capped ? p.sh.softcap * kLog2e : qk_scale * kLog2e;  // after the cap, or at once
-    const float cap_in = capped ? 2.0f * kLog2e * qk_scale / p.sh.softcap : 0.0f;
+    const bool large_cap = p.sh.softcap > kPlainCap;
+    const float to_log2 = capped ? p.sh.softcap * kLog2e : 0.0f;
+    const float score_in = capped && !large_cap ? 2.0f * kLog2e * qk_scale / p.sh.softcap : qk_scale * kLog2e;
     uint32_t cphase = 0;
     // all computing warps; what they wrote before is visible to them after it
     auto meet = [&]() -> bool {
@@ -367,10 +368,14 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
         const int lo1 = p.sh.window > 0 ? u.past + t1 + 1 - p.sh.window : 0;
         const int all_lo = p.sh.window > 0 ? max(0, kv_len - p.sh.window) : 0, all_hi = u.past + 1;
         // what a product is multiplied by: to log2 units, or to twice the cap's argument
-        float f0 = capped ? cap_in : to_log2, f1 = f0;
+        float f0 = score_in, f1 = f0;
         if (FP8) {
             f0 *= qexp[qs * BM + ra];
             f1 *= qexp[qs * BM + rb];
+        }
+        if (capped) {
+            f0 = finite(f0);
+            f1 = finite(f1);
         }
         float O[ND][4];
 #pragma unroll
@@ -501,7 +506,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                     }
                 }
                 float mx0 = FP8 ? -INFINITY : m[0], mx1 = FP8 ? -INFINITY : m[1];
-                if (capped) {
+                if (capped && !large_cap) {
 #pragma unroll
                     for (int x = 0; x < NS; ++x) {
 #pragma unroll
@@ -513,6 +518,14 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                     for (int x = 0; x < NS; ++x) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) S[x][e] *= second(e) ? f1 : f0;
+                    }
+                    if (__builtin_expect(large_cap, 0)) {
+                        float y[NS * 4];
+#pragma unroll
+                        for (int x = 0; x < NS * 4; ++x) y[x] = S[x / 4][x % 4];
+                        cap_large<NS * 4>(y, p.sh.softcap);
+#pragma unroll
+                        for (int x = 0; x < NS * 4; ++x) S[x / 4][x % 4] = y[x];
                     }
                 }
                 if (!whole) {

@@ -62,7 +62,8 @@ __device__ __forceinline__ uint64_t atoms_desc(uint32_t addr, uint32_t lead, uin
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-template <int D>
+// LARGE: the scores' cap is above kPlainCap.
+template <int D, bool LARGE>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUtensorMap map_k,
                  const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_q, const int box,
@@ -225,9 +226,9 @@ attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUt
     } else if (warp < kSoftmaxWarps) {
         // ================= softmax: thread = row =================
         const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-        const bool capped = p.sh.softcap > 0.0f;
+        const bool capped = !LARGE && p.sh.softcap > 0.0f;
         const float to_log2 = capped ? p.sh.softcap * kLog2e : p.sh.sm_scale * kLog2e;
-        const float factor = capped ? 2.0f * kLog2e * p.sh.sm_scale / p.sh.softcap : to_log2;
+        const float factor = capped ? finite(2.0f * kLog2e * p.sh.sm_scale / p.sh.softcap) : to_log2;
         unsigned char* prow = pbuf + tid * 128;
         uint32_t sphase = 0;
         auto arrive = [&](uint64_t* bar) {
@@ -274,6 +275,7 @@ attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUt
 #pragma unroll
                         for (int c = 0; c < kTile; ++c) x[c] *= factor;
                     }
+                    if (LARGE) cap_large<kTile>(x, p.sh.softcap);
                     if (!whole) {
 #pragma unroll
                         for (int c = 0; c < kTile; ++c) x[c] = pos0 + c < hi && pos0 + c >= lo ? x[c] : -INFINITY;
@@ -538,10 +540,10 @@ __global__ void __launch_bounds__(kThreads) attn_rows_join_kernel(const __grid_c
     }
 }
 
-template <int D>
+template <int D, bool LARGE>
 cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
     using Gm = RowsGeo<D>;
-    auto kern = attn_rows_kernel<D>;
+    auto kern = attn_rows_kernel<D, LARGE>;
     static_assert((4 * Gm::SLOTS + 9) * 8 + 16 * 4 <= Gm::FIXED, "small data");
     static_assert(Gm::SMEM + (kAttnMaxBatch + 1) * 4 <= 227 * 1024, "shared memory");
     int dev, sms;
@@ -596,10 +598,11 @@ bool attn_rows_supported(int d, bool fp8, int page_size, int rows) {
 }
 
 cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t stream) {
+    const bool large = a.sh.softcap > kPlainCap;
     switch (a.sh.d) {
-        case 64: return launch<64>(a, stream);
-        case 128: return launch<128>(a, stream);
-        case 256: return launch<256>(a, stream);
+        case 64: return large ? launch<64, true>(a, stream) : launch<64, false>(a, stream);
+        case 128: return large ? launch<128, true>(a, stream) : launch<128, false>(a, stream);
+        case 256: return large ? launch<256, true>(a, stream) : launch<256, false>(a, stream);
     }
     return cudaErrorInvalidValue;
 }

@@ -378,7 +378,7 @@ typedef struct {
     float norm_offset;        /* the norm's weight is norm_offset + w (0, or 1 for weights stored around zero) */
     float rope_scale;         /* factor on cos and sin (long-context scaling); 0 selects 1 */
     float sm_scale;           /* factor on q.k; 0 selects 1/sqrt(d) */
-    float softcap;            /* 0: none; c: a score x becomes c tanh(x / c) */
+    float softcap;            /* 0: none; c: a score x becomes c tanh(x / c), off by c 2^-21 at most (c <= 64), else x 2^-20 */
     float k_scale, v_scale;   /* e4m3: a stored value times this is the value; 0 selects 1. bf16: 0 or 1 */
 } gdn_attn_config;
 
