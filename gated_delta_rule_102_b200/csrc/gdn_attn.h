@@ -78,6 +78,17 @@ constexpr int kAttnMaxCtas = 192;
 constexpr int kAttnCounters = 3 * kAttnMaxCtas;  // arrivals at units, and at groups of their pieces
 constexpr size_t kAttnPartialAt = kAttnCounters * sizeof(unsigned int) + kAttnMaxCtas * sizeof(Piece);  // workspace offset
 constexpr int kAttnMaxBatch = 2048;
+// Places of the schedule (a unit's token tiles and what it costs beside them) of one sequence that fills
+// its table row, or its window, for either kernel; a batch's are numbered in 32 bits.
+constexpr long kAttnMaxPlaces = (1L << 31) - (1L << 16);
+constexpr int kAttnUnitPlaces = 13;  // a tile at the window's edge, and more than either kernel's cost of a unit
+long attn_decode_places(const AttnShape& sh, const PagedCache& c, int T);
+long attn_rows_places(const AttnShape& sh, const PagedCache& c, int T);
+inline long attn_places(const AttnShape& sh, const PagedCache& c, int T, int tile, int row_tile) {
+    long positions = (long)c.max_pages * sh.page_size;
+    if (sh.window > 0 && (long)sh.window + T < positions) positions = (long)sh.window + T;
+    return ((positions + tile - 1) / tile + kAttnUnitPlaces) * ((T * sh.G + row_tile - 1) / row_tile) * sh.Hkv;
+}
 size_t attn_workspace_bytes(int d, bool fp8, int page_size, int rows);
 
 cudaError_t launch_qk_rope_append(const AppendArgs& a, cudaStream_t stream);

@@ -173,13 +173,18 @@ gdn_status gdn_attn_decode(const gdn_attn_config* cfg, const gdn_kv_cache* cache
     if ((st = check_heads(q, &a.q)) != GDN_OK) return st;
     if (gate && (st = check_heads(gate, &a.gate)) != GDN_OK) return st;
     if (!slots || !out || !workspace) return GDN_ERR_INVALID_ARGUMENT;
+    // (a broadcast row or head, stride 0, has no tensor map: the kernel for few rows takes it, whose
+    // partial results are smaller)
+    const int rows = T * a.sh.G;
+    const bool broadcast = (a.q.row == 0 && total_tokens > 1) || (a.q.head == 0 && a.sh.Hq > 1);
+    const bool many = gdn::attn_rows_supported(a.sh.d, a.sh.fp8, a.sh.page_size, rows) && !broadcast;
+    // the kernels number the batch's work (token tiles of a row tile of a head) in 32 bits; the host knows
+    // the lengths' bound only
+    if (B * (many ? gdn::attn_rows_places(a.sh, a.c, T) : gdn::attn_decode_places(a.sh, a.c, T)) > gdn::kAttnMaxPlaces)
+        return GDN_ERR_UNSUPPORTED;
     if (misaligned(out, 16) || misaligned(lse, 4) || misaligned(slots, 4) || misaligned(err_flag, 4) ||
         misaligned(workspace, 16))
         return GDN_ERR_MISALIGNED;
-    // the kernels number the batch's work (token tiles of a row tile of a head) in 32 bits
-    const int rows = T * a.sh.G;
-    const double tiles = (double)B * (ceil((double)a.c.max_pages * a.sh.page_size / 16) + 16) * a.sh.Hkv * ((rows + 15) / 16);
-    if (tiles > 2.0e9) return GDN_ERR_UNSUPPORTED;
     a.B = B;
     a.T = T;
     a.total = total_tokens;
@@ -192,10 +197,6 @@ gdn_status gdn_attn_decode(const gdn_attn_config* cfg, const gdn_kv_cache* cache
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     a.split = reinterpret_cast<gdn::Piece*>(ws + gdn::kAttnCounters * sizeof(unsigned int));
     a.partial = reinterpret_cast<float*>(ws + gdn::kAttnPartialAt);
-    // (a broadcast row or head, stride 0, has no tensor map: the kernel for few rows takes it, whose
-    // partial results are smaller)
-    const bool broadcast = (a.q.row == 0 && total_tokens > 1) || (a.q.head == 0 && a.sh.Hq > 1);
-    const bool many = gdn::attn_rows_supported(a.sh.d, a.sh.fp8, a.sh.page_size, rows) && !broadcast;
     return from_cuda(many ? gdn::launch_attn_rows(a, (cudaStream_t)stream) : gdn::launch_attn_decode(a, (cudaStream_t)stream));
 }
 

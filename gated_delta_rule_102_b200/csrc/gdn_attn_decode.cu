@@ -1001,6 +1001,12 @@ size_t attn_workspace_bytes(int d, bool fp8, int page_size, int rows) {
     return kAttnPartialAt + (size_t)kAttnMaxCtas * 2 * tile * (d + 2) * sizeof(float);
 }
 
+long attn_decode_places(const AttnShape& sh, const PagedCache& c, int T) {
+    static_assert(kShortCost < kAttnUnitPlaces && kUnitCost < kAttnUnitPlaces, "places of a unit");
+    const int groups = row_groups(T * sh.G);
+    return attn_places(sh, c, T, Geo<64, true, 0>::HALF / (sh.d * (sh.fp8 ? 1 : 2)), groups ? 16 * groups : 8);
+}
+
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t stream) {
     switch (a.sh.d) {
         case 64: return a.sh.fp8 ? launch_rows<64, true>(a, stream) : launch_rows<64, false>(a, stream);

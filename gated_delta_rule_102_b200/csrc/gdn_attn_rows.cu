@@ -597,6 +597,11 @@ bool attn_rows_supported(int d, bool fp8, int page_size, int rows) {
     return !fp8 && page_size % 8 == 0 && rows > few;
 }
 
+long attn_rows_places(const AttnShape& sh, const PagedCache& c, int T) {
+    static_assert(kCost < kAttnUnitPlaces, "places of a unit");
+    return attn_places(sh, c, T, kTile, kRowTile / sh.G * sh.G);
+}
+
 cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t stream) {
     const bool large = a.sh.softcap > kPlainCap;
     switch (a.sh.d) {

@@ -438,7 +438,12 @@ gdn_status gdn_qk_rope_append(const gdn_attn_config* cfg, const gdn_kv_cache* ca
  *            outputs are unspecified.
  * Values of keys and values past a sequence's end are never used (they may be NaN), and
  * a non-finite value of a later drafted token does not reach the rows before it. Pages
- * that lie wholly before every row's window are not read. B <= 2048. Results do not
+ * that lie wholly before every row's window are not read. B <= 2048, and B times a
+ * sequence's places at most 2^31 - 2^16 (GDN_ERR_UNSUPPORTED): its places are Hkv x (row
+ * tiles) x (token tiles + 13), of max_pages * page_size tokens (or window + T, if fewer) in
+ * tiles of 8192 / (d * element bytes), and of T * Hq / Hkv rows in tiles of 8, 16, 32 or 64
+ * (the smallest that holds them, else 64); with many rows tiles are 64 tokens by 128 rows
+ * (rounded down to a multiple of Hq / Hkv). Results do not
  * depend on timing: the split of the work and the order of every sum follow from the
  * lengths alone. A sequence with a flagged page has unspecified outputs.
  */
