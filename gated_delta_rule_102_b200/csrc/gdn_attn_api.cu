@@ -93,6 +93,7 @@ gdn_status check_tables(int32_t page_size, int32_t n, const int32_t* table, int3
     if (page_size <= 0 || n < 0 || rows <= 0 || max_pages <= 0 || num_pages <= 0) return GDN_ERR_INVALID_ARGUMENT;
     if (n > gdn::kPagesMaxBatch || page_size > 65536 || (long)max_pages * page_size > 0x7fffffffL)
         return GDN_ERR_UNSUPPORTED;
+    if (num_pages > gdn::kPagesMost || max_pages > gdn::kPagesMost) return GDN_ERR_UNSUPPORTED;
     if (n == 0) return GDN_OK;
     if (!table || !refs) return GDN_ERR_INVALID_ARGUMENT;
     if (misaligned(table, 4) || misaligned(refs, 4) || misaligned(err_flag, 4)) return GDN_ERR_MISALIGNED;

@@ -3,7 +3,7 @@ the check of alignment that follows it and are refused there (so nothing is enqu
 import pytest
 import torch
 
-from test_attn_abi_cpu import MIS, ODD4, UNS, L, attn, cache, cfg, heads  # noqa: F401
+from test_attn_abi_cpu import FAKE, MIS, ODD2, ODD4, UNS, L, attn, cache, cfg, heads  # noqa: F401
 
 LIMIT = 2 ** 31 - 2 ** 16
 
@@ -59,3 +59,16 @@ def test_short_sequences_in_wide_tables_are_served(L):
     c = cfg(num_q_heads=128, num_kv_heads=8, head_dim=128, page_size=64, rotary_dim=0)
     assert attn(L, c, cache(max_pages=131072 // 64), B=2048, T=16, q=heads(row=128 * 128, head=128), out=ODD4) == MIS
     assert attn(L, c, cache(max_pages=262144 // 64), B=1024, T=16, q=heads(row=128 * 128, head=128), out=ODD4) == MIS
+
+
+def test_pools_and_tables_that_32_bits_can_walk(L):
+    """Page numbers and table entries are walked in strides: past 2^30 a stride would leave 32 bits."""
+    F, most = FAKE, 1 << 30
+    calls = dict(reserve=lambda pages, width: L.gdn_pages_reserve(1, 2, F, F, 1, F, 4, width, F, F, pages, ODD2, None),
+                 fork=lambda pages, width: L.gdn_pages_fork(1, 2, F, F, F, 4, width, F, F, pages, F, F, ODD2, None),
+                 free=lambda pages, width: L.gdn_pages_free(2, F, F, 4, width, F, F, pages, ODD2, None),
+                 compact=lambda pages, width: L.gdn_pages_compact(F, 4, width, F, pages, F, F, F, F, ODD2, None))
+    for name, call in calls.items():
+        assert call(most, 8) == MIS and call(8, most) == MIS, name
+        assert call(most + 1, 8) == UNS and call((1 << 31) - 1, 8) == UNS, name
+        assert call(8, most + 1) == UNS and call(8, (1 << 31) - 1) == UNS, name
