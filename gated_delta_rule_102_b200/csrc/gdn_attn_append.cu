@@ -229,6 +229,7 @@ __global__ void __launch_bounds__(kMostThreads, 2) qk_rope_append_kernel(const A
     const int past = __ldg(p.c.seq_lens + slot);
     if (past < 0 || past > p.c.max_pages * p.sh.page_size - n) {
         if (report) atomicOr(p.err_flag, GDN_DEVICE_ERR_SEQLEN_BIT);
+        asm volatile("cp.async.wait_all;\n" ::: "memory");  // the words on their way land before the CTA's memory is another's
         return;
     }
     if (tid < rows) {
