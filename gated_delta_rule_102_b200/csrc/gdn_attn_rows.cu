@@ -86,7 +86,8 @@ attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUt
     uint64_t* qfull = pvdone + 1;       // a unit's queries are there
     uint64_t* qfree = qfull + 1;        // its scores are all formed
     uint64_t* sbar = qfree + 1;         // the softmax warps' own barrier
-    int* misc = reinterpret_cast<int*>(sbar + 1);  // [16] sums; 8, 9: tile skipped by the products; 10: TMEM; 15: stop
+    uint64_t* drain = sbar + 1;         // every product is complete
+    int* misc = reinterpret_cast<int*>(drain + 1);  // [16] sums; 8, 9: tile skipped by the products; 10: TMEM; 15: stop
     int* prefix = misc + 16;                       // [B + 1]
     volatile int* stop = misc + 15;
     volatile int* skip = misc + 8;
@@ -110,6 +111,7 @@ attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUt
         mbar_init(qfull, 1);
         mbar_init(qfree, 1);
         mbar_init(sbar, kSoftmaxWarps);
+        mbar_init(drain, 1);
         *stop = 0;
         mbar_init_fence();
         fence_proxy_async_smem();
@@ -221,6 +223,9 @@ attn_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUt
                 }
                 if (ok) ok = accumulate(n - 1);
             }
+            // also where a wait ran out, here or in another role: nothing runs when the tensor memory goes back
+            umma_commit(smem_addr(drain));
+            mbar_wait_bounded(drain, 0);
         }
         __syncwarp();
     } else if (warp < kSoftmaxWarps) {
@@ -544,7 +549,7 @@ template <int D, bool LARGE>
 cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
     using Gm = RowsGeo<D>;
     auto kern = attn_rows_kernel<D, LARGE>;
-    static_assert((4 * Gm::SLOTS + 9) * 8 + 16 * 4 <= Gm::FIXED, "small data");
+    static_assert((4 * Gm::SLOTS + 10) * 8 + 16 * 4 <= Gm::FIXED, "small data");
     static_assert(Gm::SMEM + (kAttnMaxBatch + 1) * 4 <= 227 * 1024, "shared memory");
     int dev, sms;
     cudaError_t e = device_sms(&dev, &sms);
