@@ -20,6 +20,13 @@ GDN_DEVICE_ERR_PAGE = 16
 GDN_KV_BF16, GDN_KV_E4M3 = 0, 1
 
 
+def _i32(x, what: str) -> int:
+    """x, if 32 bits hold it: ctypes takes the low 32 bits of any other number without a word."""
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{what}: {x} does not fit 32 bits")
+    return x
+
+
 class GdnAttnConfig(ctypes.Structure):
     """Mirror of ``gdn_attn_config``."""
     _fields_ = [(n, ctypes.c_int32) for n in ("num_q_heads", "num_kv_heads", "head_dim", "rotary_dim", "rope_interleaved",
@@ -35,6 +42,9 @@ class GdnAttnConfig(ctypes.Structure):
                  GDN_KV_E4M3: GDN_KV_E4M3}
         if kv_dtype not in kinds:
             raise TypeError(f"kv_dtype: {kv_dtype}, expected torch.bfloat16 or torch.float8_e4m3fn")
+        for n, x in (("num_q_heads", num_q_heads), ("num_kv_heads", num_kv_heads), ("head_dim", head_dim),
+                     ("rotary_dim", rotary_dim), ("page_size", page_size), ("window", window)):
+            _i32(x, n)
         return cls(num_q_heads, num_kv_heads, head_dim, rotary_dim, int(bool(rope_interleaved)), page_size,
                    kinds[kv_dtype], window, norm_eps, norm_offset, rope_scale, sm_scale, softcap, k_scale, v_scale)
 
@@ -94,7 +104,8 @@ class _Call:
         # a handle of its own without argument types: the values below need no conversion at each launch
         self.fn = ctypes.CFUNCTYPE(ctypes.c_int32)(ctypes.cast(declared, ctypes.c_void_p).value)
         self.name, self.keep, self.device = name, keep, device
-        self.args = tuple(t(x) if t in (ctypes.c_void_p, ctypes.c_int32) else (t() if x is None else x)
+        self.args = tuple(t(_i32(x, name)) if t is ctypes.c_int32 else
+                          (t(x) if t is ctypes.c_void_p else (t() if x is None else x))
                           for t, x in zip(declared.argtypes, args))
         self.others = torch.cuda.device_count() > 1
 
@@ -210,6 +221,8 @@ def _cache(a: _Args, cfg, k_pages, v_pages, page_table, seq_lens):
     shape = (k_pages.shape[0], cfg.page_size, cfg.num_kv_heads, cfg.head_dim)
     if page_table.dim() != 2:
         raise ValueError("page_table: expected [rows][max_pages]")
+    for n in (k_pages.shape[0], *page_table.shape):
+        _i32(n, a.name)
     c = _KvCache(a.ptr(k_pages, kinds, "k_pages", shape), a.ptr(v_pages, kinds, "v_pages", shape), k_pages.shape[0],
                  a.ptr(page_table, _I32, "page_table"), page_table.shape[0], page_table.shape[1],
                  a.ptr(seq_lens, _I32, "seq_lens", (page_table.shape[0],)))
@@ -267,7 +280,7 @@ def gdn_attn_decode(cfg: GdnAttnConfig, q, k_pages, v_pages, page_table, seq_len
 
 
 def attn_decode_workspace_bytes(cfg: GdnAttnConfig, B: int, T: int) -> int:
-    return int(_lib().gdn_attn_decode_workspace_bytes(ctypes.byref(cfg), B, T))
+    return int(_lib().gdn_attn_decode_workspace_bytes(ctypes.byref(cfg), _i32(B, "B"), _i32(T, "T")))
 
 
 def attn_decode_workspace(cfg: GdnAttnConfig, B: int, T: int, device) -> torch.Tensor:
@@ -279,6 +292,8 @@ def gdn_rope_inv_freq_host(rotary_dim: int, theta: float, factor: float = 1.0, y
                            original_len: int = 0):
     """(inv_freq [rotary_dim / 2] as a CPU tensor, rope_scale): rotation speeds, optionally
     slowed down for contexts `factor` times the trained length."""
+    _i32(rotary_dim, "rotary_dim")
+    _i32(original_len, "original_len")
     f = torch.empty(max(rotary_dim // 2, 0), dtype=torch.float32)
     scale = ctypes.c_float()
     st = _lib().gdn_rope_inv_freq_host(rotary_dim, theta, factor, int(yarn), original_len, f.data_ptr(), ctypes.byref(scale))
