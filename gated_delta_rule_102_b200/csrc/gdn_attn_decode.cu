@@ -759,7 +759,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                         for (int e = 0; e < 2; ++e)
                             *reinterpret_cast<float2*>(part + (e ? rb : ra) * JPITCH + x * 8 + 2 * j) = make_float2(o[2 * e], o[2 * e + 1]);
                     } else if (x % 2 == 0) {  // tile x has the even columns, tile x + 1 the odd ones
-                        const float(&o1)[4] = O[round * RND + x + 1 - 2 * (x & 1)];
+                        const float(&o1)[4] = O[round * RND + (x | 1)];
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
                             *reinterpret_cast<float4*>(part + (e ? rb : ra) * JPITCH + x * 8 + 4 * j) = make_float4(o[2 * e], o1[2 * e], o[2 * e + 1], o1[2 * e + 1]);
@@ -938,7 +938,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
     }
 
     static_assert(BM * (kJoinMost + 2) * 4 <= SLOTS * Gm::SLOTB, "weights");
-    join_units<D, FP8, BM, kComputeWarps * 32>(p, pieces + NQ, split_first, split_last, BM, reinterpret_cast<float*>(ring), misc + 12, meet);
+    join_units<D, FP8, BM, kComputeWarps * 32>(p, pieces + NQ, split_first, split_last, reinterpret_cast<float*>(ring), misc + 12, meet);
 }
 
 template <int D, bool FP8, int WM>

@@ -366,10 +366,10 @@ __device__ __forceinline__ void write_out4(const AttnArgs& p, size_t row, int he
 // then the groups: at 74 pieces of 8 KB one CTA alone would read 600 KB.
 // All NT threads that meet() joins, after each has written its part of the pieces.
 // shared_pieces: the share's first and last split piece; wt: BM * (kJoinMost + 2) floats and
-// flag: one int of shared memory. row_tile: query rows of a unit (BM, or fewer).
+// flag: one int of shared memory.
 template <int D, bool FP8, int BM, int NT, typename Meet>
 __device__ __forceinline__ bool join_units(const AttnArgs& p, const Piece* shared_pieces, bool split_first, bool split_last,
-                                           int row_tile, float* wt, volatile int* flag, Meet meet) {
+                                           float* wt, volatile int* flag, Meet meet) {
     constexpr int WP = kJoinMost + 2, PSTRIDE = BM * (D + 2);
     const int tid = threadIdx.x, G = p.sh.G, inv_g = 65536 / G + 1;  // r / G = r * inv_g >> 16 for r < 320, G <= 16
     if (!split_first && !split_last) return true;
@@ -378,7 +378,7 @@ __device__ __forceinline__ bool join_units(const AttnArgs& p, const Piece* share
     for (int which = 0; which < 2; ++which) {
         if (!(which ? split_last : split_first)) continue;
         const Piece u = shared_pieces[which];
-        const int rows = min(row_tile, u.n * G - u.rt * row_tile), all = u.c1 - u.c0 + 1;
+        const int rows = min(BM, u.n * G - u.rt * BM), all = u.c1 - u.c0 + 1;
         auto place_of = [&](int i) { return p.partial + (size_t)((u.c0 + i) * 2 + (i == 0)) * PSTRIDE; };
         const bool flat = all <= kJoinFlat;
         for (int level = flat ? 1 : 0; level < 2; ++level) {
@@ -415,14 +415,14 @@ __device__ __forceinline__ bool join_units(const AttnArgs& p, const Piece* share
             }
             if (!meet()) return false;
             // four columns by kItems rows a thread, so that their loads are in flight together
-            constexpr int kItems = BM == 128 ? 8 : (BM > 16 ? 4 : 2), kPieces = BM == 128 ? 3 : 4;
+            constexpr int kItems = BM > 16 ? 4 : 2, kPieces = 4;
             const int items = rows * (D / 4);
             for (int k0 = tid; k0 < items; k0 += kItems * NT) {
                 float4 o[kItems];
                 uint2 z[kItems];
 #pragma unroll
                 for (int y = 0; y < kItems; ++y) {
-                    const int k = k0 + y * NT, r = k / (D / 4), rr = u.rt * row_tile + r, t = (rr * inv_g) >> 16;
+                    const int k = k0 + y * NT, r = k / (D / 4), rr = u.rt * BM + r, t = (rr * inv_g) >> 16;
                     o[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     z[y] = make_uint2(0, 0);
                     if (p.gate.ptr && level == 1 && k < items) z[y] = gate_of4(p, (size_t)u.first + t, u.h * G + rr - t * G, (k % (D / 4)) * 4);
@@ -461,7 +461,7 @@ __device__ __forceinline__ bool join_units(const AttnArgs& p, const Piece* share
                         continue;
                     }
                     const int r = k / (D / 4), col = (k % (D / 4)) * 4;
-                    const int rr = u.rt * row_tile + r, t = (rr * inv_g) >> 16, head = u.h * G + rr - t * G;
+                    const int rr = u.rt * BM + r, t = (rr * inv_g) >> 16, head = u.h * G + rr - t * G;
                     const size_t row = (size_t)u.first + t;
                     const float* w = wt + r * WP;
                     write_out4<FP8>(p, row, head, D, col, o[y], 1.0f / w[kJoinMost], z[y]);
