@@ -12,11 +12,13 @@
 // shared memory. Everything is fp32 and rounded once, on the way out; the angle is formed in
 // 64 bits and in turns (a 32-bit product is off by a thousandth of a radian at position 10^4
 // already), only its fraction goes to the 32-bit sine and cosine.
-// Bound by HBM at many rows, where instructions come close (about 200 a warp and row), and by
-// the latency of the dependent lookups at few. Measured: 256 sequences of 16 rows, 16 query and 2
-// key/value heads of 256, bf16: 18.2 us for 84 MB (4.6 TB/s); 200 sequences of up to 16 rows, 32
-// and 8 heads of 128 to e4m3: 16.8 us (more than 300 instructions a warp and row, and CTAs of
-// unequal rows); one row 3.1 us.
+// Measured: 256 sequences of 16 rows, 16 query and 2 key/value heads of 256, bf16: 18.5 us for 84 MB
+// (4.5 TB/s), 256 equal CTAs on 148 SMs, of which 108 have two and 40 one; about 200 instructions a warp
+// and row. 200 sequences of up to 16 rows, 32 and 8 heads of 128 to e4m3: 16.9 us where the bytes take 5.6
+// and the instructions (430 a warp and row, set-up among them) 7: the 400 CTAs have 1 to 8 rows each or
+// none, so that an SM is without work for a third of the time, and while it has some the chain of a row
+// (its words, the norm's shuffles, the rotation, the store) leaves half of the issue slots empty. One row
+// takes 3.3 us, dependent lookups.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

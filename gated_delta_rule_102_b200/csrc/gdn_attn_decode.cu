@@ -214,8 +214,9 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                 continue;
             }
             if (!to_convert) break;
-            // e4m3 keys become fp16, so the queries do too: a power of two per row brings its
-            // largest element to 2^14 .. 2^15, exact for every element above 2^-38 of that
+            // e4m3 keys become fp16, so the queries do too: a power of two per row brings its largest
+            // element to 2^14 .. 2^15. Elements down to 2^-31 of that stay exact (eight bits above fp16's
+            // smallest, 2^-24), smaller ones are off by 2^-39 of it at most.
             constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes a row, rows at a time
             const int qs = converted % NQ;
             if (!wait(qraw + qs, (converted / NQ) & 1)) break;
@@ -575,8 +576,11 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
                     }
                 }
 
-                // a slot that some rows may not see in full: a value that is not finite must not reach
-                // the rows whose mask leaves it out (0 * inf), so such slots go token by token
+                // The probabilities meet the values in the 16 bits that the products take, rounded once: bf16
+                // with a bf16 cache (by 2^-8 of each at most; the row's largest so far is 1, exact), fp16 with
+                // an e4m3 one (2^-11). The sums are of the unrounded ones.
+                // A slot that some rows may not see in full: a value that is not finite must not reach
+                // the rows whose mask leaves it out (0 * inf), so such slots go token by token.
                 bool plain = true;
                 if (!whole) {
                     bool bad = false;

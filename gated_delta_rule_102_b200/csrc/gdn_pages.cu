@@ -8,7 +8,8 @@
 // stops as soon as enough are found; a second launch over the whole GPU does the part that
 // does not (copying table rows, renumbering entries). The work is a few dependent passes
 // over small arrays: bound by latency, not bandwidth (free, fork and reserve of 2 children: 8 us
-// together). The copies are bound by HBM: 2000 pages' moves, 262 MB each way, 46 us.
+// together). The copies are bound by HBM: 500 moves in a pool of 2000 pages (four buffers of 64 KB a
+// page, 131 MB read and as many written) take 46 us, 5.7 TB/s.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

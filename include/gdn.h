@@ -350,7 +350,9 @@ size_t gdn_decode_static_scratch_bytes(void);
  *   too, and neither changes seq_lens, so every layer of the step sees the same lengths;
  *   the caller advances them once per step (by the accepted count after a speculative
  *   step: positions past seq_lens are rewritten by the next append, which is all that
- *   rewinding takes).
+ *   rewinding takes. A sequence that was forked, or is a fork, is not rewound below the
+ *   last page boundary at or before the length that it then had: pages before that are
+ *   shared, and an append to them would write into every holder's).
  * Rows. With cu_seqlens NULL sequence i owns T token rows i*T ..; otherwise T is the
  *   largest count (1..16) and sequence i owns rows cu_seqlens[i] .. cu_seqlens[i+1]-1,
  *   as in gdn_decode_step_varlen (0 tokens: left untouched, which also serves padded
