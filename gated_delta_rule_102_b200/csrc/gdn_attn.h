@@ -115,7 +115,8 @@ struct PageArgs {
     int32_t* err_flag;
 };
 constexpr int kPagesMaxBatch = 2048;
-constexpr int kPagesMost = 1 << 30;  // pages, and entries of a table row: the kernels walk both in 32 bits, up to 2^14 at a time
+// Pages, and entries of a table row, at most: the kernels walk both in 32 bits, up to 2^14 at a time.
+constexpr int kPagesMost = 0x7fffffff - (1 << 15);
 cudaError_t launch_pages_reserve(const PageArgs& a, cudaStream_t stream);
 cudaError_t launch_pages_fork(const PageArgs& a, cudaStream_t stream);
 cudaError_t launch_pages_free(const PageArgs& a, cudaStream_t stream);

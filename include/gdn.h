@@ -480,7 +480,7 @@ gdn_status gdn_rope_inv_freq_host(int32_t rotary_dim, double theta, double facto
  * GDN_DEVICE_ERR_SEQLEN, and GDN_DEVICE_ERR_PAGE flags a sequence that was skipped
  * because no free page was left for it (then every later one of the call that needs
  * pages is skipped too) or because its table row is in use.
- * n (sequences of a call) <= 2048, num_pages and max_pages <= 2^30.
+ * n (sequences of a call) <= 2048, num_pages and max_pages < 2^31 - 2^15.
  *
  * reserve: gives slot i the pages for its next n_tokens[i] tokens (n_tokens NULL: T).
  * fork:    child dst[i] becomes a copy of parent src[i]: whole pages are shared, a

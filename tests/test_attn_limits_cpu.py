@@ -62,8 +62,8 @@ def test_short_sequences_in_wide_tables_are_served(L):
 
 
 def test_pools_and_tables_that_32_bits_can_walk(L):
-    """Page numbers and table entries are walked in strides: past 2^30 a stride would leave 32 bits."""
-    F, most = FAKE, 1 << 30
+    """Page numbers and table entries are walked in strides: within a stride of 2^31 an index would leave 32 bits."""
+    F, most = FAKE, (1 << 31) - 1 - (1 << 15)
     calls = dict(reserve=lambda pages, width: L.gdn_pages_reserve(1, 2, F, F, 1, F, 4, width, F, F, pages, ODD2, None),
                  fork=lambda pages, width: L.gdn_pages_fork(1, 2, F, F, F, 4, width, F, F, pages, F, F, ODD2, None),
                  free=lambda pages, width: L.gdn_pages_free(2, F, F, 4, width, F, F, pages, ODD2, None),
