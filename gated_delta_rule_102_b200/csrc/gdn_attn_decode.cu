@@ -249,9 +249,12 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
             if (lane == 0) mbar_arrive(qfull + qs);
             ++converted;
         }
-        // after an abort: what is in flight lands before the block leaves
-        if (*stop != 0) {
-            for (int i = FP8 ? converted : max(0, sent - NQ); i < sent; ++i) mbar_wait_bounded((FP8 ? qraw : qfull) + i % NQ, (i / NQ) & 1);
+        // What is in flight lands before the block leaves, which it may at any time now: a role whose wait
+        // ran out does not wait for this one. What was read has landed (and its place may be turns ahead, where
+        // the phase's parity says nothing any more).
+        for (int i = FP8 ? converted : max(0, sent - NQ); i < sent; ++i) {
+            auto was_read = [&] { return load_acquire(qfreed + i % NQ) >= (i / NQ + 1) * kComputeWarps; };
+            if (!was_read()) mbar_wait_deadline((FP8 ? qraw : qfull) + i % NQ, (i / NQ) & 1, kWaitTimeoutCycles, was_read);
         }
         return;
     }
@@ -319,8 +322,13 @@ attn_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ C
             if (more_slots) find_tokens();
         }
         cp_wait_all();
-        if (*stop != 0 && box) {  // as above
-            for (int i = sent; i >= 0 && i > sent - SLOTS; i -= kLoadWarps) mbar_wait_bounded(full + i % SLOTS, (i / SLOTS) & 1);
+        if (box) {  // as above: a place's slot of the turn that has not been read, if this warp has filled it
+#pragma unroll 1
+            for (int st = 0; st < SLOTS; ++st) {
+                const int turn = load_acquire(freed + st) / Gm::READERS, i = turn * SLOTS + st;
+                auto was_read = [&] { return load_acquire(freed + st) >= (turn + 1) * Gm::READERS; };
+                if (i <= sent && i % kLoadWarps == pw) mbar_wait_deadline(full + st, turn & 1, kWaitTimeoutCycles, was_read);
+            }
         }
         return;
     }
